@@ -267,7 +267,8 @@ def _own_write(s):
 
 def _cache_plan(s):
     import free_block_sparse_mean_b200 as sa
-    return sa.CachePlan(table=s["table"], lens=s["lens"], starts=s["starts"], granted=s["new"], mask=s.get("mask"))
+    return sa.CachePlan(table=s["table"], lens=s["lens"], starts=s["starts"], granted=s["new"], mask=s.get("mask"),
+                        max_new=s["case"]["new"])
 
 
 def _own_tree(s):
