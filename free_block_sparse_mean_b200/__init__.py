@@ -9,6 +9,9 @@ torch stream. PyTorch provides device memory and streams, nothing else.
     o = sparse_attn_fwd(q, k, v, plan, lam=-12.0)      # stage 2: sparse attention
 
 q, k, v: bf16 CUDA tensors [B, H, N, d], contiguous, d in {64, 128}.
+
+What follows a prompt runs over a paged cache (cache.py): sparse_attn_cache_plan,
+sparse_attn_cache_write, sparse_attn_tree_fwd and sparse_attn_cache_accept.
 """
 from __future__ import annotations
 
@@ -30,6 +33,8 @@ __all__ = ["Plan", "sparse_attn_plan", "sparse_attn_fwd", "sparse_attn_fwd_recal
            "sparse_attn_plan_workspace_size", "sparse_attn_num_tiles", "sparse_attn_device_error",
            "sparse_attn_host_workspace_size",
            "sparse_attn_selftest_wait_timeout",
+           "CachePlan", "sparse_attn_cache_plan", "sparse_attn_cache_write", "sparse_attn_tree_workspace_size",
+           "sparse_attn_tree_fwd", "sparse_attn_cache_accept",
            "SparseAttnError", "BLOCK"]
 
 
@@ -461,3 +466,7 @@ def sparse_attn_selftest_wait_timeout(limit_us: int, device=None) -> None:
     dev = torch.device("cuda") if device is None else torch.device(device)
     with torch.cuda.device(dev):
         _call("sparse_attn_selftest_wait_timeout", lib.sparse_attn_selftest_wait_timeout(int(limit_us), _stream(dev)))
+
+
+from .cache import (CachePlan, sparse_attn_cache_accept, sparse_attn_cache_plan,  # noqa: E402
+                    sparse_attn_cache_write, sparse_attn_tree_fwd, sparse_attn_tree_workspace_size)

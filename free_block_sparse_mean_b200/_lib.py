@@ -15,6 +15,8 @@ SA_FILTER_LAMBDA = 0
 SA_FILTER_RECALL = 1
 SA_HOST_FP8_SCORES = 1
 SA_HOST_INT8_SCORES = 2
+SA_BF16 = 0
+SA_F16 = 1
 STATUS_NAMES = {
     0: "SA_OK",
     1: "SA_ERR_INVALID_ARG",
@@ -46,12 +48,30 @@ EXPORTS = (
     "sparse_attn_cluster",
     "sparse_attn_permute_rows",
     "sparse_attn_selftest_wait_timeout",
+    "sparse_attn_cache_plan",
+    "sparse_attn_cache_write",
+    "sparse_attn_tree_workspace_size",
+    "sparse_attn_tree_fwd",
+    "sparse_attn_cache_accept",
 )
 
 
 class SaShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class SaCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class SaStep(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("n", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("words", ctypes.c_int32), ("starts", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("granted", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p)]
 
 
 class SparseAttnError(RuntimeError):
@@ -120,5 +140,16 @@ def load(path: str = LIB_PATH):
     lib.sparse_attn_permute_rows.restype = i32
     lib.sparse_attn_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.sparse_attn_selftest_wait_timeout.restype = i32
+    i64 = ctypes.c_int64
+    lib.sparse_attn_cache_plan.argtypes = [vp] * 7 + [i32] * 6 + [vp] * 8
+    lib.sparse_attn_cache_plan.restype = i32
+    lib.sparse_attn_cache_write.argtypes = [vp, vp, i64, i64, i32, vp, vp, vp, SaCache, vp]
+    lib.sparse_attn_cache_write.restype = i32
+    lib.sparse_attn_tree_workspace_size.argtypes = [SaCache, SaStep, i32]
+    lib.sparse_attn_tree_workspace_size.restype = sz
+    lib.sparse_attn_tree_fwd.argtypes = [vp, i64, i64, i32, vp, vp, SaCache, SaStep, f32, vp, i64, i64, vp, vp, sz, vp]
+    lib.sparse_attn_tree_fwd.restype = i32
+    lib.sparse_attn_cache_accept.argtypes = [vp, vp, SaCache, i32, i64, SaStep, vp, i32, vp, vp]
+    lib.sparse_attn_cache_accept.restype = i32
     _lib = lib
     return lib

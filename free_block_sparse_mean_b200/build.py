@@ -11,7 +11,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", "sa_api.cu"), os.path.join(HERE, "csrc", "sa_noalloc.cu")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("sa_api.cu", "sa_noalloc.cu", "sa_cache.cu")]
 OUT = os.path.join(HERE, "libsparse_attn.so")
 DEPS = [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join(HERE, "csrc"))] + \
        [os.path.join(ROOT, "include", "sparse_attn.h")]

@@ -220,6 +220,7 @@ sa_status launch_cluster(const sa_shape& s, const void* X, const void* Y, int it
 
 namespace sa {
 cudaError_t take_noalloc_device_error(cudaStream_t st, unsigned int* out);   // sa_noalloc.cu
+cudaError_t take_cache_device_error(cudaStream_t st, unsigned int* out);     // sa_cache.cu
 
 // Exercises the device-side failure path: one warp waits on an mbarrier whose
 // phase nothing completes, through the same bounded wait the pipelines use, with
@@ -666,9 +667,10 @@ sa_status sparse_attn_device_error(void* stream, int32_t* code) {
       cudaSuccess)
     return SA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return SA_ERR_CUDA;
-  unsigned int w = 0;   // the other translation unit's word (see sa_noalloc.cu)
+  unsigned int w = 0, x = 0;   // the other translation units' words (sa_noalloc.cu, sa_cache.cu)
   if (sa::take_noalloc_device_error(st, &w) != cudaSuccess) return SA_ERR_CUDA;
-  *code = static_cast<int32_t>(v | w);
+  if (sa::take_cache_device_error(st, &x) != cudaSuccess) return SA_ERR_CUDA;
+  *code = static_cast<int32_t>(v | w | x);
   return SA_OK;
 }
 

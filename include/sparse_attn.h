@@ -364,6 +364,143 @@ sa_status sparse_attn_plan_noalloc(const void* Q, const void* K, sa_shape s, flo
  * SA_ERR_CUDA. */
 sa_status sparse_attn_selftest_wait_timeout(uint32_t limit_us, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Paged cache: decoding and drafting steps over cached keys and values.
+ *
+ * What follows a prompt: new tokens of several requests (one each, a tree of drafted
+ * tokens each, or a chunk of a prompt) attend to the tokens their requests have in a
+ * cache and to one another. A cache is a pool of pages of page_size tokens; request
+ * r's token at place t lies in page table[r][t / page_size], and its slot is
+ * page_id * page_size + t % page_size. A step is
+ *
+ *   sparse_attn_cache_plan    once: pages for the new tokens, slots, positions, masks
+ *   sparse_attn_cache_write   per layer: the new keys and values into their slots
+ *   sparse_attn_tree_fwd      per layer: the attention of the new tokens
+ *   sparse_attn_cache_accept  once, all layers: the accepted drafts to their places
+ *
+ * Everything a step depends on is read on the GPU, so a captured graph of these calls
+ * can be replayed with other lengths, counts and trees in the same buffers. Numbers
+ * on the GPU cannot be checked on the host: what is out of range is skipped as each
+ * call says, and sets bit 2 (a count, length or parent) or bit 1 (a page id or slot)
+ * of the device error word. Arrays of one call must not overlap unless said. The
+ * conventions at the top of this file hold (ownership, streams, errors). */
+typedef enum { SA_BF16 = 0, SA_F16 = 1 } sa_dtype;
+
+/* A pool of pages for keys or values: element (page, token, head, i) lies at
+ * page*page_stride + token*token_stride + head*head_stride + i (elements; both
+ * [pages][page_size][Hkv][d] and [pages][Hkv][page_size][d] fit). Strides are
+ * positive multiples of 8 (head_stride is not read for Hkv = 1), base 16-byte
+ * aligned. Keys and values have one description and two bases. */
+typedef struct {
+  int32_t pages;         /* pages in the pool; pages*page_size < 2^31 */
+  int32_t page_size;     /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t Hkv;           /* key heads */
+  int32_t d;             /* 64 or 128 */
+  int32_t dtype;         /* SA_BF16 or SA_F16, of Q, O and both caches */
+  int64_t page_stride, token_stride, head_stride;
+} sa_cache;
+
+/* The requests of a step, device arrays (4-byte aligned) and host sizes. */
+typedef struct {
+  int32_t R;               /* requests, 1..8192 */
+  int32_t n;               /* rows of the step's token buffers */
+  int32_t width;           /* columns of table; R*width, width*page_size < 2^31 */
+  int32_t max_new;         /* the most new tokens of a request, or 0 if not known. It only
+                              sizes the tiles: more tokens than this are still right */
+  int32_t words;           /* words of a mask row, 1..32, or 0 with mask = NULL */
+  const int32_t* starts;   /* [R+1]: request r's new tokens are rows starts[r]..starts[r+1]-1 */
+  const int32_t* lens;     /* [R]: its tokens in the cache before them */
+  const int32_t* granted;  /* [R] or NULL: only its first granted[r] new tokens exist */
+  const int32_t* table;    /* [R][width] page ids */
+  const uint32_t* mask;    /* [n][words] or NULL: bit j of row starts[r]+i is set if new token
+                              i of the request sees its new token j (any bits, none included);
+                              NULL: it sees new tokens 0..i */
+} sa_step;
+
+/* Plans a step: pages, block table, slot map, positions and tree masks from the
+ * requests' lengths, in one launch.
+ *
+ *   lens        [R] tokens in the cache
+ *   new_tokens  [R] new tokens of the step, 0 included; a negative count means that the
+ *               request has ended: its held pages go back on the free list
+ *   held        [R] pages in the request's table row (held*page_size >= lens; a step whose
+ *               drafts were not all accepted leaves pages that the next one uses first)
+ *   nfree       [1] ids in free_pages
+ *   free_pages  [pages] in/out: the free list, entries 0..nfree-1. Ended requests' pages are
+ *               appended in request order; pages are taken from the end, in request order
+ *   table       [R][width] in/out: columns held.. get the pages taken
+ *   parents     [n] or NULL: parent of each new token among its request's (index < its own, -1
+ *               for none), in rows order; NULL: each follows the one before it
+ *   n           rows of the outputs per token
+ *   words       words of a mask row (1..32), or 0 with mask = NULL (parents needs a mask)
+ *   held_out    [R], nfree_out [1]: the counts after the step (must not be the inputs)
+ *   starts      [R+1]: first row of each request's new tokens; starts[R] <= n
+ *   granted     [R]: new_tokens of a request that got its pages, else 0. Requests are
+ *               served in order while the list (returned pages included) covers the sum of
+ *               their needs; one that needs no page is always served
+ *   slots       [n]: slot of each new token; -1 for rows of requests not served and behind
+ *               the last one
+ *   positions   [n]: lens + depth in the tree (lens + index without parents), 0 behind
+ *   mask        [n][words]: bit j set if new token j is the token itself or an ancestor
+ *
+ * Not served, with bit 2 set: a request whose counts are out of range (held above width
+ * or too few for lens, negative lens, more tokens than width pages or 32*words
+ * bits hold, rows past n). A parent out of range ends that walk and sets bit 2. The
+ * call may be repeated with the same inputs and gives the same outputs. Errors:
+ * SA_ERR_INVALID_ARG (NULL, misaligned, sizes below 1), SA_ERR_UNSUPPORTED (R > 8192,
+ * page_size, a product of sizes above 2^31 - 1), SA_ERR_CUDA. */
+sa_status sparse_attn_cache_plan(const int32_t* lens, const int32_t* new_tokens, const int32_t* held,
+                                 const int32_t* nfree, int32_t* free_pages, int32_t* table, const int32_t* parents,
+                                 int32_t R, int32_t pages, int32_t page_size, int32_t width, int32_t n,
+                                 int32_t words, int32_t* held_out, int32_t* nfree_out, int32_t* starts,
+                                 int32_t* granted, int32_t* slots, int32_t* positions, uint32_t* mask,
+                                 void* stream);
+
+/* Writes n rows of keys and values [n][Hkv][d] (strides in elements, multiples of 8,
+ * shared by K and V; a stride of a dimension of one is not read) to their slots of the
+ * caches. A row of slot -1 is left out; another slot outside the pool is left out and
+ * sets bit 1. Slots other than -1 must differ: of two rows with one slot either
+ * one's 16-byte pieces may stay. */
+sa_status sparse_attn_cache_write(const void* K, const void* V, int64_t token_stride, int64_t head_stride, int32_t n,
+                                  const int32_t* slots, void* K_cache, void* V_cache, sa_cache c, void* stream);
+
+/* Attention of the step's new tokens: for row i of request r and query head h (key
+ * head h / (Hq/Hkv)), O[i][h] = softmax over the request's cached tokens and the new
+ * ones that i sees of scale * q.k, times V. The new tokens' keys and values are in the
+ * cache already (sparse_attn_cache_write). Scores, softmax and sums are fp32; P is
+ * rounded to the type for P.V.
+ *
+ *   Q, O       [n][Hq][d] with their strides (elements, multiples of 8), Hq a multiple of
+ *              c.Hkv, at most 128 query heads to a key head
+ *   scale      finite, > 0
+ *   lse        [n][Hq] or NULL: natural log of the softmax sum, -inf where nothing is seen
+ *   workspace  at least sparse_attn_tree_workspace_size bytes, 256-byte aligned; calls that
+ *              may run at once need one each (so do two graphs replayed together)
+ *
+ * A row that sees nothing is written as 0. Rows of tokens that do not exist (behind a
+ * request's granted ones or behind the last request) are left as they were. What lies in
+ * cached pages behind a request's last token, and keys and values of new tokens in rows
+ * that do not see them, never reach a result, infinities and NaN included. A request with
+ * counts out of range is skipped (bit 2); a page id out of range is read as page 0 (bit 1).
+ * Results do not depend on timing; the number of pieces a row's keys are cut into, and so
+ * the rounding, depends on the lengths of all requests of the call. Errors: as
+ * sparse_attn_fwd, and SA_ERR_WORKSPACE. */
+size_t sparse_attn_tree_workspace_size(sa_cache c, sa_step s, int32_t Hq);
+sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, int32_t Hq, const void* K_cache,
+                               const void* V_cache, sa_cache c, sa_step s, float scale, void* O, int64_t o_token,
+                               int64_t o_head, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Moves the accepted new tokens of each request to the places behind its cached ones:
+ * with a = accepted[r], the rows of K and V at place lens[r] + a[i] go to place lens[r] + i
+ * for i < taken[r], in every layer (layer l's caches lie l*layer_stride elements behind the
+ * bases). accepted is [R][cols], a[0] < a[1] < ... < the request's new tokens, cols <=
+ * 1024; 0 <= taken[r] <= cols. The new length of the request is lens[r] + taken[r]. A
+ * request whose numbers are out of range keeps its rows and sets bit 2 (a page id: bit 1).
+ * The pages of two requests in one call must differ from place lens on. */
+sa_status sparse_attn_cache_accept(void* K_cache, void* V_cache, sa_cache c, int32_t layers, int64_t layer_stride,
+                                   sa_step s, const int32_t* accepted, int32_t cols, const int32_t* taken,
+                                   void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* sparse_attn_status_string(sa_status st);
 
