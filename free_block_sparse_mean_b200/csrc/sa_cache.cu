@@ -18,8 +18,8 @@
 namespace {
 
 constexpr int kSMs = 148;                       // B200
-constexpr int kTreeTarget = 2 * kSMs;           // pieces aimed at: two CTAs on every SM
-constexpr int kTreeMinBlocks = 2;               // smallest piece, in 64-key blocks
+constexpr int kTreeCtas = 2 * kSMs;             // two CTAs on every SM share the call's key blocks
+constexpr int kTreeMinBlocks = 2;               // smallest share of a CTA, in 64-key blocks
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
@@ -111,39 +111,32 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, const sa_cache& c) {
 // The tiling and workspace of sparse_attn_tree_fwd, from what the host knows.
 struct TreeLayout {
   int G, TT;
-  bool split;                 // some tile may have more than one piece
-  int64_t tiles;              // most (tile, key head) pairs
-  int64_t slots;              // most pieces of tiles with more than one
-  size_t part_o, part_ml, sched, total;
+  bool split;                 // the border between two CTAs' shares may cut a tile
+  size_t part_o, part_ml, line, total;
 };
 TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   TreeLayout L{};
   L.G = Hq / c.Hkv;
   L.TT = 128 / L.G;
-  const int most = s.max_new > 0 ? std::min(s.max_new, s.n) : s.n;
-  L.TT = std::min(L.TT, most);
-  // sum of ceil(T / TT) over the requests
-  L.tiles = std::min<int64_t>(s.n, static_cast<int64_t>(s.n) / L.TT + std::min(s.R, s.n)) * c.Hkv;
-  L.split = static_cast<int64_t>(s.width) * c.page_size > int64_t{64} * kTreeMinBlocks;
-  // pieces of length C of a tile of nb > C blocks: ceil(nb / C) <= 2 nb / C, and <= nb / C + 1
-  L.slots = L.split ? std::min<int64_t>(2 * kTreeTarget, kTreeTarget + L.tiles) : 0;
-  const size_t rows = static_cast<size_t>(L.slots) * L.TT * L.G;
+  L.TT = std::min(L.TT, s.max_new > 0 ? std::min(s.max_new, s.n) : s.n);
+  L.split = static_cast<int64_t>(s.width) * c.page_size > sa::kBlock;
+  const size_t rows = L.split ? size_t{2} * kTreeCtas * L.TT * L.G : 0;
   size_t o = 0;
   L.part_o = o; o += al(rows * c.d * sizeof(float));
   L.part_ml = o; o += al(rows * sizeof(float2));
-  L.sched = o; o += L.split ? al(static_cast<size_t>(s.R) * sizeof(int2)) : 0;
+  L.line = o; o += L.split ? al((static_cast<size_t>(s.R) + 2) * sizeof(long long)) : 0;
   L.total = o;
   return L;
 }
 
 template <int D, int kElem, bool kSmallQ>
 sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const sa::TreeArgs& a,
-                      const void* V, const sa_cache& c, unsigned grid, bool split, cudaStream_t st) {
+                      const void* V, const sa_cache& c, bool split, cudaStream_t st) {
   using Cfg = sa::TreeCfg<D, kSmallQ>;
   auto kern = sa::tree_fwd_kernel<D, kElem, kSmallQ>;
   if (sa::set_smem(kern, Cfg::kSmemBytes) != SA_OK) return SA_ERR_CUDA;
-  kern<<<grid, sa::kTreeThreads, Cfg::kSmemBytes, st>>>(mq, mk, mv, a, static_cast<const uint16_t*>(V),
+  kern<<<kTreeCtas, sa::kTreeThreads, Cfg::kSmemBytes, st>>>(mq, mk, mv, a, static_cast<const uint16_t*>(V),
                                                         c.page_stride, c.token_stride, c.head_stride);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   if (split) {
@@ -287,7 +280,6 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   if (!aligned(Q, 16) || !aligned(K_cache, 16) || !aligned(V_cache, 16) || !aligned(O, 16) || !aligned(lse, 4))
     return SA_ERR_INVALID_ARG;
   const TreeLayout L = tree_layout(c, s, Hq);
-  if (L.tiles + kTreeTarget > 0x7fffffff) return SA_ERR_UNSUPPORTED;
   if (L.total > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)) return SA_ERR_WORKSPACE;
   CUtensorMap mq, mk, mv;
   if (!make_q_map(&mq, Q, q_token, q_head, s.n, Hq, c.d, L.G, L.TT) || !make_cache_map(&mk, K_cache, c) ||
@@ -309,7 +301,6 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   a.Hkv = c.Hkv;
   a.G = L.G;
   a.TT = L.TT;
-  a.target = kTreeTarget;
   a.min_blocks = kTreeMinBlocks;
   a.O = O;
   a.o_token = s.n > 1 ? o_token : 0;
@@ -319,15 +310,13 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   if (L.split) {
     a.part_o = reinterpret_cast<float*>(ws + L.part_o);
     a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
-    a.sched = reinterpret_cast<int2*>(ws + L.sched);
+    a.line = reinterpret_cast<long long*>(ws + L.line);
   }
-  // pieces: at most nb / C + 1 of each tile, whose nb / C add up to the target
-  const unsigned grid = static_cast<unsigned>(L.tiles + (L.split ? kTreeTarget : 0));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool small = L.TT * L.G <= 32, f16 = c.dtype == SA_F16;
 #define SA_TREE(D, E)                                                                      \
-  (small ? launch_tree<D, E, true>(mq, mk, mv, a, V_cache, c, grid, L.split, st)           \
-         : launch_tree<D, E, false>(mq, mk, mv, a, V_cache, c, grid, L.split, st))
+  (small ? launch_tree<D, E, true>(mq, mk, mv, a, V_cache, c, L.split, st)           \
+         : launch_tree<D, E, false>(mq, mk, mv, a, V_cache, c, L.split, st))
   if (c.d == 64) return f16 ? SA_TREE(64, sa::kElemF16) : SA_TREE(64, sa::kElemBF16);
   return f16 ? SA_TREE(128, sa::kElemF16) : SA_TREE(128, sa::kElemBF16);
 #undef SA_TREE

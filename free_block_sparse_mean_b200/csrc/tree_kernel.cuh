@@ -10,32 +10,37 @@
 // to 128 rows of (new token, head of the group), token-major: TT = 128 / G tokens.
 // One TMA box {64, G heads, TT tokens} per 128-byte column chunk brings them.
 //
-// Work. A tile's keys are cut into pieces of whole 64-key blocks; a CTA takes one
-// piece of one tile. The lengths are on the GPU, so each CTA finds its piece there:
-// all sum the requests' blocks (a scan over the requests), take the piece length
-// from that total, so that about `target` pieces exist whatever the mix of lengths,
-// and look up the piece of their own index. A tile of one piece is written to O by
-// its CTA; the others leave (max, sum, unnormalised O) in fp32 for
-// tree_combine_kernel.
+// Work. The lengths are on the GPU and ragged, so the calls' work is one line of key
+// blocks: request by request, key head by key head, tile by tile, each tile's blocks in
+// order. `ctas` CTAs (two on every SM, fewer when that leaves less than min_blocks to
+// each) take equal shares of the line, whatever tiles they run through: every CTA
+// finds its share itself, from a scan over the requests. A tile that one CTA runs from
+// end to end is written to O; of a tile cut by the border between shares each CTA
+// leaves (max, sum, unnormalised O) in fp32 for tree_combine_kernel. A CTA cuts at
+// most two tiles, one at each end of its share, so 2 * ctas such pieces are all there
+// can be. Measured against one CTA for each tile or for a fixed number of blocks: see
+// the table of target sizes in the design notes of this kernel's launch.
 //
-// Keys. Per 64-key block the load warp reads the block's page ids and issues one TMA
-// box (pages of 64 tokens and more) or one per page and column chunk (smaller
-// pages). A page id is read only where the request has tokens; places behind the
+// Keys. Per 64-key block a warp reads the block's page ids and issues one TMA box
+// (pages of 64 tokens and more) or one per page and column chunk (smaller pages). A page id is read only where the request has tokens; places behind the
 // last token in its page are masked in S by column, and their V rows are set to zero
 // in shared memory, since 0 * NaN is not 0. For the same reason V elements that are
 // not finite are taken out of blocks that some row does not see whole; the rows that
 // do see such a token get the element added at the end (see `special` below).
 //
-// Roles (224 threads): warp 0 loads, warp 1 owns TMEM and issues S = Q K^T, warp 2
-// issues O += P V, warps 3..6 run the softmax (thread = row), the O correction and the
-// epilogue; a softmax warp whose 32 rows are all empty leaves at once, so a
-// single-token call pays the exponentials of one warp. TMEM (256 columns): S [0,64),
-// P [64,96) and [96,128), O [128, 128 + D). Two CTAs fit on an SM.
+// Roles (192 threads): warp 0 loads V and issues O += P V, warp 1 owns TMEM, loads Q and
+// K and issues S = Q K^T, warps 2..5 run the softmax (thread = row), the O correction
+// and the epilogue; a softmax warp whose 32 rows do not exist only keeps the barriers'
+// counts, so a single-token call pays the exponentials of one warp. TMEM (256 columns):
+// S [0,64), P [64,96) and [96,128), O [128, 128 + D). Two CTAs fit on an SM.
 //
-// The barrier phases follow the block-sparse forward's argument: S(k+1) is issued only
-// after every active softmax warp released S(k); P(k) goes to buffer k & 1 once
-// P(k-2).V has finished; a K or V stage is refilled after the product that read it has
-// completed. So no wait is ever more than one phase behind its barrier.
+// Blocks are counted through the CTA's whole share, tiles included, and so are the
+// barrier phases: block k uses ring stage k % ST, S and P as in the block-sparse forward:
+// S(k+1) is issued only after every softmax warp released S(k); P(k) goes to buffer
+// k & 1 once P(k-2).V has finished; a stage is refilled after the product that read it
+// has completed. A tile's first P.V overwrites O: its P is published only after the
+// softmax warps have read the tile before out of TMEM. So no wait is ever more than one
+// phase behind its barrier.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -44,7 +49,7 @@
 
 namespace sa {
 
-constexpr int kTreeThreads = 224;
+constexpr int kTreeThreads = 192;
 
 // 16-bit element types of Q, K, V, P and O.
 enum Elem16 : int { kElemBF16 = 0, kElemF16 = 1 };
@@ -66,26 +71,29 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   }
 }
 
-// kSmallQ: the tile has at most 32 rows, so Q takes 32 rows of shared memory and the
-// freed space a third stage of K and of V. The S product still reads 128 rows (rows
-// behind Q are whatever lies there); a row's result touches no other row, and the
-// rows that do not exist are never written out.
+// kSmallQ: the tile has at most 32 rows, so Q takes 32 rows of shared memory (twice, so
+// that the next tile's is there early) and the freed space a third stage of K and of V.
+// The S product still reads 128 rows (rows behind Q are whatever lies there); a row's
+// result touches no other row, and the rows that do not exist are never written out.
 template <int D, bool kSmallQ>
 struct TreeCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kQRows = kSmallQ ? 32 : 128;
+  static constexpr int kQBufs = kSmallQ ? 2 : 1;
   static constexpr int kQChunkBytes = kQRows * 128;
+  static constexpr int kQBytes = kChunks * kQChunkBytes;
   static constexpr int kKVChunkBytes = kBlock * 128;
   static constexpr int kKVBytes = kChunks * kKVChunkBytes;
   static constexpr int ST = D == 64 ? (kSmallQ ? 6 : 5) : (kSmallQ ? 3 : 2);   // stages of K and of V
   static constexpr int oQ = 0;
-  static constexpr int oK = oQ + kChunks * kQChunkBytes;
+  static constexpr int oK = oQ + kQBufs * kQBytes;
   static constexpr int oV = oK + ST * kKVBytes;
   static constexpr int oBar = oV + ST * kKVBytes;
-  static constexpr int kNumBars = 4 * ST + 8;
+  static constexpr int kNumBars = 4 * ST + kQBufs + 7;
   static constexpr int oMisc = oBar + kNumBars * 8;
-  static constexpr int kSmemBytes = oMisc + 512 + 1024;
+  static constexpr int kSmemBytes = oMisc + 512;
   static constexpr uint32_t kColS = 0, kColP0 = 64, kColP1 = 96, kColO = 128, kTmemCols = 256;
+  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs on an SM");
 };
 
 struct TreeArgs {
@@ -93,14 +101,14 @@ struct TreeArgs {
   const uint32_t* mask;           // [n][words] or null
   int R, n, width, pages, page_shift, words;
   int Hkv, G, TT;                 // key heads, query heads each, tokens of a tile
-  int target, min_blocks;         // pieces aimed at, smallest piece in blocks
+  int min_blocks;                 // smallest share of a CTA, in blocks
   void* O;
   long long o_token, o_head;      // strides in elements
   float* lse;                     // [n][Hkv * G] or null
   float scale_log2;
-  float* part_o;                  // [slot][tile rows][D]
-  float2* part_ml;                // [slot][tile rows]
-  int2* sched;                    // per request: pieces (0 or 1: nothing to combine), first slot
+  float* part_o;                  // [2 * CTA + (0: the piece ends its tile, or 1: begins it)][tile rows][D]
+  float2* part_ml;                // [as part_o][tile rows]
+  long long* line;                // [R + 2]: each request's first block on the line, the line's length, `ctas`
 };
 
 struct TreeReq {
@@ -133,9 +141,40 @@ __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int r, bool* 
 __device__ __forceinline__ int tree_tile_blocks(const TreeReq& q, int tile, int TT, bool masked) {
   return masked ? q.nb : (q.L + min(q.T, (tile + 1) * TT) + kBlock - 1) / kBlock;
 }
-// First block of piece p of `pieces` over nb blocks.
-__device__ __forceinline__ int tree_piece_start(int nb, int p, int pieces) {
-  return static_cast<int>(static_cast<long long>(nb) * p / pieces);
+
+// sum of floor((a i + b) / m) over i = 0 .. n-1 (a, b >= 0, m > 0), by the Euclidean
+// reduction: take whole parts out of a and b, then count the lattice points the other way.
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// Blocks of a key head's first `tiles` tiles of a request.
+__device__ __forceinline__ long long tree_blocks_before(const TreeReq& q, int tiles, int TT, bool masked) {
+  if (tiles <= 0) return 0;
+  if (masked) return static_cast<long long>(tiles) * q.nb;
+  const int full = min(tiles, q.tiles - 1);            // the last tile may hold fewer tokens
+  const long long s = full > 0 ? floor_sum(full, kBlock, TT, q.L + TT + kBlock - 1) : 0;
+  return tiles == q.tiles ? s + q.nb : s;
+}
+
+// The share of the line that CTA c of `ctas` takes begins here.
+__device__ __forceinline__ long long tree_share(long long total, int c, int ctas) { return total * c / ctas; }
+// The CTA whose share holds block x of the line.
+__device__ __forceinline__ int tree_owner(long long total, long long x, int ctas) {
+  return static_cast<int>(((x + 1) * ctas + total - 1) / total) - 1;
 }
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v,
@@ -191,6 +230,101 @@ __device__ __forceinline__ float to_float16(uint32_t bits) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
 }
 
+// A walk along a CTA's share of the line, tile by tile: the piece of the current tile
+// is its blocks [b0, b0 + n). A piece that begins inside its tile is kept for the end, so
+// that every CTA begins with block 0 of some tile: the CTAs on one key head then read the
+// same keys at about the same time, from L2. In the line's order a prompt's chunk (2 x
+// 2,048 tokens behind 30,000, 8 key heads) took 1,622 us, DRAM bound at 9 GB a call.
+struct TreeWalk {
+  int r, head, tile, b0, n, nbt;
+  TreeReq q;
+  long long left;                 // blocks of the share from this piece on, the kept piece aside
+  int kr, khead, ktile, kb0;      // the kept piece (kr = -1: none)
+
+  __device__ __forceinline__ void cut(const TreeArgs& a) {
+    nbt = tree_tile_blocks(q, tile, a.TT, a.mask != nullptr);
+    n = static_cast<int>(min(left, static_cast<long long>(nbt - b0)));
+  }
+  // The first piece, from the share's first block (r, head, tile, b0, q and left set).
+  __device__ __forceinline__ void begin(const TreeArgs& a) {
+    cut(a);
+    kr = -1;
+    if (b0 > 0 && n < left) {
+      const int first = r;
+      khead = head;
+      ktile = tile;
+      kb0 = b0;
+      next(a);
+      kr = first;
+    }
+  }
+  // To the next piece of the share; false at its end.
+  __device__ __forceinline__ bool next(const TreeArgs& a) {
+    left -= n;
+    bool bad;
+    if (left <= 0) {
+      if (kr < 0) return false;
+      r = kr;
+      head = khead;
+      tile = ktile;
+      b0 = kb0;
+      q = tree_request(a, r, &bad);
+      nbt = tree_tile_blocks(q, tile, a.TT, a.mask != nullptr);
+      n = nbt - b0;
+      left = n;
+      kr = -1;
+      return true;
+    }
+    b0 = 0;
+    if (++tile == q.tiles) {
+      tile = 0;
+      if (++head == a.Hkv) {
+        head = 0;
+        do {
+          if (++r >= a.R) return false;       // (not reached while the lengths stay as they were)
+          q = tree_request(a, r, &bad);
+        } while (q.T == 0);
+      }
+    }
+    cut(a);
+    return true;
+  }
+};
+
+// A walk block by block, for the loads, with the lane's page of the current block
+// fetched one block ahead.
+struct TreeLoad {
+  TreeWalk w;
+  int k;                          // block of the piece
+  bool more;
+  int id;                         // this lane's page of it, -1: nothing to load
+  const int* row;
+  __device__ __forceinline__ void fetch(const TreeArgs& a, bool loads, int off, bool* bad) {
+    id = -1;
+    if (!more) return;
+    const int at = (w.b0 + k) * kBlock + off;
+    if (!loads || at >= w.q.L + w.q.T) return;
+    id = row[at >> a.page_shift];
+    if (id < 0 || id >= a.pages) {
+      *bad = true;
+      id = 0;                     // flagged; any page of the pool keeps the load in bounds
+    }
+  }
+  __device__ __forceinline__ void begin(const TreeArgs& a, const TreeWalk& from) {
+    w = from;
+    k = 0;
+    more = true;
+    row = a.table + static_cast<long long>(w.r) * a.width;
+  }
+  __device__ __forceinline__ void step(const TreeArgs& a) {
+    if (++k == w.n) {
+      k = 0;
+      more = w.next(a);
+      row = a.table + static_cast<long long>(w.r) * a.width;
+    }
+  }
+};
+
 template <int D, int kElem, bool kSmallQ>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     tree_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -199,8 +333,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   using C = TreeCfg<D, kSmallQ>;
   constexpr uint32_t kIdescS = idesc_16_f32(kElem, 128, 64, false);
   constexpr uint32_t kIdescPV = idesc_16_f32(kElem, 128, D, true);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kWarps = kTreeThreads / 32;
+  extern __shared__ __align__(1024) uint8_t tree_smem[];
+  uint8_t* base = tree_smem;
+  if (smem_u32(base) & 1023u) {               // the swizzled tiles need it; the kernel has no static shared memory
+    if (threadIdx.x == 0) atomicOr(&g_dev_error, DEVERR_VALUE);
+    return;
+  }
   uint8_t* sQ = base + C::oQ;
   uint8_t* sK = base + C::oK;
   uint8_t* sV = base + C::oV;
@@ -209,125 +348,24 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   uint64_t* kempty = kfull + C::ST;        // [ST] K stage consumed by S MMA
   uint64_t* vfull = kempty + C::ST;        // [ST] V stage loaded
   uint64_t* vempty = vfull + C::ST;        // [ST] V stage consumed by P.V MMA
-  uint64_t* q_full = vempty + C::ST;       // Q tile loaded
-  uint64_t* s_full = q_full + 1;           // S(k) written by the MMA (phase k)
-  uint64_t* s_free = q_full + 2;           // S(k) read by the active softmax warps (phase k)
-  uint64_t* p_full = q_full + 3;           // [2] by k parity: P(k) in TMEM and O corrected
-  uint64_t* pv_done = q_full + 5;          // [2] by k parity: P(k).V finished
-  uint64_t* drain = q_full + 7;            // every MMA of the tile finished, `special` written
+  uint64_t* q_full = vempty + C::ST;       // [kQBufs] Q of a tile loaded
+  uint64_t* s_full = q_full + C::kQBufs;   // S(k) written by the MMA (phase k)
+  uint64_t* s_free = s_full + 1;           // S(k) read by the softmax warps (phase k)
+  uint64_t* p_full = s_full + 2;           // [2] by k parity: P(k) in TMEM and O corrected
+  uint64_t* pv_done = s_full + 4;          // [2] by k parity: P(k).V finished (the MMA and `special`)
+  uint64_t* drain = s_full + 6;            // every MMA of the CTA finished
   int* misc = reinterpret_cast<int*>(base + C::oMisc);
   volatile int* abort_flag = misc + 0;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 1);
-  volatile int* special = misc + 2;        // an element of V was taken out (not finite)
-  int* found = misc + 4;                   // this CTA's piece: request, index in it, pieces, slot
-  long long* wsum = reinterpret_cast<long long*>(misc + 16);   // [7 warps][2]
+  volatile int* special = misc + 2;        // [2] by tile parity: 1 + a tile of which an element of V was taken out
+  int* found = misc + 4;                   // the share's first request, its T and L
+  long long* found_at = reinterpret_cast<long long*>(misc + 8);   // the request's first block on the line
+  long long* wsum = reinterpret_cast<long long*>(misc + 16);      // [kWarps]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned FULL = 0xffffffffu;
 
-  // ------------------------------------------------------------ find this CTA's piece
-  bool bad = false;
-  TreeReq mine{0, 0, 0, 0};
-  long long total = 0;
-  for (int r = threadIdx.x; r < a.R; r += kTreeThreads) {
-    mine = tree_request(a, r, &bad);
-    total += static_cast<long long>(mine.tiles) * mine.nb;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(FULL, total, o);
-  if (lane == 0) wsum[warp] = total;
-  if (threadIdx.x == 0) {
-    found[0] = -1;
-    *abort_flag = 0;
-    *special = 0;
-  }
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kTreeThreads / 32; ++w) total += wsum[w];
-  total *= a.Hkv;
-  const int piece_blocks =
-      static_cast<int>(max(static_cast<long long>(a.min_blocks), (total + a.target - 1) / a.target));
-  __syncthreads();
-  long long items_before = 0, slots_before = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kTreeThreads) {
-    const int r = r0 + threadIdx.x;
-    if (a.R > kTreeThreads) {
-      bool again = false;
-      mine = r < a.R ? tree_request(a, r, &again) : TreeReq{0, 0, 0, 0};
-    }
-    const int pieces = (mine.nb + piece_blocks - 1) / piece_blocks;
-    const long long items = static_cast<long long>(mine.tiles) * pieces * a.Hkv;
-    const long long slots = pieces > 1 ? items : 0;
-    long long ii = items, ss = slots;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(FULL, ii, o), y = __shfl_up_sync(FULL, ss, o);
-      if (lane >= o) {
-        ii += x;
-        ss += y;
-      }
-    }
-    if (lane == 31) {
-      wsum[2 * warp] = ii;
-      wsum[2 * warp + 1] = ss;
-    }
-    __syncthreads();
-    long long all_i = 0, all_s = 0;
-#pragma unroll
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
-      if (w == warp) {
-        ii += items_before + all_i;
-        ss += slots_before + all_s;
-      }
-      all_i += wsum[2 * w];
-      all_s += wsum[2 * w + 1];
-    }
-    const long long first = ii - items, slot = ss - slots;
-    if (items > 0 && blockIdx.x >= first && blockIdx.x < ii) {
-      found[0] = r;
-      found[1] = static_cast<int>(blockIdx.x - first);
-      found[2] = pieces;
-      found[3] = static_cast<int>(slot);
-      found[4] = mine.T;
-      found[5] = mine.L;
-    }
-    if (blockIdx.x == 0 && a.sched && r < a.R) a.sched[r] = make_int2(pieces, static_cast<int>(slot));
-    items_before += all_i;
-    slots_before += all_s;
-    __syncthreads();
-    if (found[0] >= 0 && blockIdx.x != 0) break;
-  }
-  if (blockIdx.x == 0 && bad) atomicOr(&g_dev_error, DEVERR_VALUE);
-  if (found[0] < 0) return;
-  const int req = found[0];
-  const int pieces = found[2];
-  TreeReq rq;
-  rq.T = found[4];
-  rq.L = found[5];
-  rq.nb = (rq.L + rq.T + kBlock - 1) / kBlock;
-  rq.tiles = (rq.T + a.TT - 1) / a.TT;
-  // tiles change fastest, so that the CTAs that run together share the keys they read
-  int rest = found[1];
-  const int tile = rq.tiles - 1 - rest % rq.tiles;
-  rest /= rq.tiles;
-  const int piece = rest % pieces, head = rest / pieces;
-  const bool masked = a.mask != nullptr;
-  const int nbt = tree_tile_blocks(rq, tile, a.TT, masked);
-  const int b0 = tree_piece_start(rq.nb, piece, pieces);
-  const int b1 = min(nbt, tree_piece_start(rq.nb, piece + 1, pieces));
-  const int n = b1 - b0;
-  if (n <= 0) return;                                   // only past a tile's last key: nothing is combined from here
-  const int t0 = tile * a.TT;
-  const int rows = min(a.TT, rq.T - t0) * a.G;          // rows of the tile that exist
-  const int nact = (rows + 31) >> 5;                    // softmax warps with rows
-  const int keys = rq.L + rq.T;
-  // every row sees the keys before `open`; from there on rows differ
-  const int open = masked ? rq.L : rq.L + t0 + 1;
-  const int* trow = a.table + static_cast<long long>(req) * a.width;
-  const long long tok0 = static_cast<long long>(a.starts[req]) + t0;
-  const int page = 1 << a.page_shift;
-
+  // ------------------------------------------------------------ set up, find this CTA's share
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&kfull[s], 1);
@@ -335,199 +373,335 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(&vfull[s], 1);
       mbar_init(&vempty[s], 1);
     }
-    mbar_init(q_full, 1);
+    for (int b = 0; b < C::kQBufs; ++b) mbar_init(&q_full[b], 1);
     mbar_init(s_full, 1);
-    mbar_init(s_free, nact);
-    mbar_init(&p_full[0], nact);
-    mbar_init(&p_full[1], nact);
-    mbar_init(&pv_done[0], 1);
-    mbar_init(&pv_done[1], 1);
-    mbar_init(drain, 3);
+    mbar_init(s_free, 4);
+    mbar_init(&p_full[0], 4);
+    mbar_init(&p_full[1], 4);
+    mbar_init(&pv_done[0], 2);
+    mbar_init(&pv_done[1], 2);
+    mbar_init(drain, 2);
     fence_mbar_init();
+    *abort_flag = 0;
+    special[0] = 0;
+    special[1] = 0;
+    found[0] = -1;
   }
+  bool bad = false;
+  const bool masked = a.mask != nullptr;
+  TreeReq mine{0, 0, 0, 0};
+  long long blocks = 0, total = 0;            // of the thread's request, of all
+  for (int r = threadIdx.x; r < a.R; r += kTreeThreads) {
+    mine = tree_request(a, r, &bad);
+    blocks = tree_blocks_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
+    total += blocks;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(FULL, total, o);
+  if (lane == 0) wsum[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += wsum[w];
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + a.min_blocks - 1) / a.min_blocks));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.line) {
+    a.line[a.R] = total;
+    a.line[a.R + 1] = ctas;
+  }
+  if (blockIdx.x == 0 && bad) atomicOr(&g_dev_error, DEVERR_VALUE);
+  const int cta = static_cast<int>(blockIdx.x);
+  if (cta >= max(ctas, 1)) return;
+  const long long share0 = ctas > 0 ? tree_share(total, cta, ctas) : 0;
+  const long long share1 = ctas > 0 ? tree_share(total, cta + 1, ctas) : 0;
+  __syncthreads();
+  long long before = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kTreeThreads) {
+    const int r = r0 + threadIdx.x;
+    if (a.R > kTreeThreads) {
+      bool again;
+      mine = r < a.R ? tree_request(a, r, &again) : TreeReq{0, 0, 0, 0};
+      blocks = r < a.R ? tree_blocks_before(mine, mine.tiles, a.TT, masked) * a.Hkv : 0;
+    }
+    long long upto = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(FULL, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) wsum[warp] = upto;
+    __syncthreads();
+    upto += before;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += wsum[w];
+      before += wsum[w];
+    }
+    const long long at = upto - blocks;
+    if (blocks > 0 && share0 >= at && share0 < upto) {
+      found[0] = r;
+      found[1] = mine.T;
+      found[2] = mine.L;
+      *found_at = at;
+    }
+    if (cta == 0 && a.line && r < a.R) a.line[r] = at;
+    __syncthreads();
+    if (found[0] >= 0 && cta != 0) break;
+  }
+  if (found[0] < 0) return;                   // no work at all
+  TreeWalk walk;
+  walk.r = found[0];
+  walk.q.T = found[1];
+  walk.q.L = found[2];
+  walk.q.nb = (walk.q.L + walk.q.T + kBlock - 1) / kBlock;
+  walk.q.tiles = (walk.q.T + a.TT - 1) / a.TT;
+  walk.left = share1 - share0;
+  {
+    const long long per_head = tree_blocks_before(walk.q, walk.q.tiles, a.TT, masked);
+    long long x = share0 - *found_at;
+    walk.head = static_cast<int>(x / per_head);
+    x -= walk.head * per_head;
+    int lo = 0, hi = walk.q.tiles;            // the last tile that begins at or before x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tree_blocks_before(walk.q, mid, a.TT, masked) <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    walk.tile = lo;
+    walk.b0 = static_cast<int>(x - tree_blocks_before(walk.q, lo, a.TT, masked));
+    walk.begin(a);
+  }
+  const int page = 1 << a.page_shift;
+  // a block is 64 / sub boxes of `sub` tokens; below 64 tokens a box holds one
+  // 128-byte column chunk (lane = chunk * boxes + box), else the whole block
+  const int sub_shift = min(a.page_shift, 6), sub = 1 << sub_shift;
+  const int subs = kBlock >> sub_shift;
+  const int my_sub = lane & (subs - 1), my_chunk = lane >> (6 - sub_shift);
+  const bool loads = subs == 1 ? lane == 0 : my_chunk < C::kChunks;
+  const int sub_off = my_sub * sub, dst_off = my_chunk * C::kKVChunkBytes + sub_off * 128;
+
   if (warp == 1) tmem_alloc(tmem_holder, C::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      mbar_expect_tx(q_full, C::kChunks * a.TT * a.G * 128);
-#pragma unroll
-      for (int c = 0; c < C::kChunks; ++c)
-        tma_load_4d(sQ + c * C::kQChunkBytes, &tmQ, 0, head * a.G, static_cast<int>(tok0), c, q_full);
-    }
-    // a block is 64 / sub boxes of `sub` tokens; below 64 tokens a box holds one
-    // 128-byte column chunk (lane = chunk * boxes + box), else the whole block
-    const int sub_shift = min(a.page_shift, 6), sub = 1 << sub_shift;
-    const int subs = kBlock >> sub_shift;
-    const bool whole = subs == 1;
-    const int my_sub = lane & (subs - 1), my_chunk = lane >> (6 - sub_shift);
-    const bool loads = whole ? lane == 0 : my_chunk < C::kChunks;
-    const int box_bytes = sub * 128 * (whole ? C::kChunks : 1);
-    const int dst_off = my_chunk * C::kKVChunkBytes + my_sub * sub * 128;
+  if (warp < 2) {
+    // Both issue warps run the same ring: stage k % ST holds block k of the share, loaded
+    // when the product that read block k - ST has completed.
+    const bool is_v = warp == 0;
+    uint8_t* ring = is_v ? sV : sK;
+    uint64_t* full = is_v ? vfull : kfull;
+    uint64_t* empty = is_v ? vempty : kempty;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
+    if (lane == 0) tma_prefetch_desc(map);
     bool bad_page = false;
-    auto page_of = [&](int k) {      // this lane's page of block k, -1 past the last token
-      const int at = (b0 + k) * kBlock + my_sub * sub;
-      if (k >= n || !loads || at >= keys) return -1;
-      int id = trow[at >> a.page_shift];
-      if (id < 0 || id >= a.pages) {
-        bad_page = true;
-        id = 0;                      // flagged; any page of the pool keeps the load in bounds
-      }
-      return id;
+    TreeLoad ld;
+    ld.begin(a, walk);
+    ld.fetch(a, loads, sub_off, &bad_page);
+    int issued = 0;
+    auto load_next = [&]() {
+      const int s = issued % C::ST;
+      const int kb = (ld.w.b0 + ld.k) * kBlock;
+      const int boxes = (min(ld.w.q.L + ld.w.q.T - kb, kBlock) + sub - 1) >> sub_shift;
+      if (lane == 0) mbar_expect_tx(&full[s], static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks);
+      __syncwarp();
+      if (ld.id >= 0)
+        tma_load_5d(ring + s * C::kKVBytes + dst_off, map, 0, (kb + sub_off) & (page - 1), my_chunk, ld.w.head, ld.id,
+                    &full[s]);
+      ++issued;
+      ld.step(a);
+      ld.fetch(a, loads, sub_off, &bad_page);
     };
-    int id = page_of(0);
+    for (int s = 0; s < C::ST && ld.more; ++s) load_next();
+    const uint32_t ring_a = smem_u32(ring);
+    int k = 0;                                  // blocks of the share
     bool ok = true;
-    int k = 0;
-    for (; k < n; ++k) {
-      const int next_id = page_of(k + 1);
-      const int s = k % C::ST;
-      const uint32_t ph = static_cast<uint32_t>(k / C::ST - 1) & 1u;
-      const int kb = (b0 + k) * kBlock;
-      const int boxes = (min(keys - kb, kBlock) + sub - 1) >> sub_shift;
-      const uint32_t bytes = static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks;
-      const int y = (kb + my_sub * sub) & (page - 1);
-      if (k >= C::ST) ok = warp_wait(&kempty[s], ph, abort_flag);
-      if (!ok) break;
-      if (lane == 0) mbar_expect_tx(&kfull[s], bytes);
-      __syncwarp();
-      if (id >= 0) tma_load_5d(sK + s * C::kKVBytes + dst_off, &tmK, 0, y, my_chunk, head, id, &kfull[s]);
-      if (k >= C::ST) ok = warp_wait(&vempty[s], ph, abort_flag);
-      if (!ok) break;
-      if (lane == 0) mbar_expect_tx(&vfull[s], bytes);
-      __syncwarp();
-      if (id >= 0) tma_load_5d(sV + s * C::kKVBytes + dst_off, &tmV, 0, y, my_chunk, head, id, &vfull[s]);
-      id = next_id;
-    }
-    if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
-    (void)box_bytes;
-    // every load that was issued has landed before the CTA leaves (bounded)
-    if (lane == 0) {
-      mbar_wait_drain(q_full, 0u);
-      for (int kk = max(0, k - C::ST); kk < k; ++kk) {
-        mbar_wait_drain(&kfull[kk % C::ST], static_cast<uint32_t>(kk / C::ST) & 1u);
-        mbar_wait_drain(&vfull[kk % C::ST], static_cast<uint32_t>(kk / C::ST) & 1u);
-      }
-      // K(k) may have been issued without V(k)
-      if (!ok && k < n) {
-        const int s = k % C::ST;
-        mbar_wait_drain(&kfull[s], static_cast<uint32_t>(k / C::ST) & 1u);
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S issuer
-    if (lane == 0) {
-      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
-      bool ok = mbar_wait(q_full, 0u, abort_flag);
-      for (int k = 0; ok && k < n; ++k) {
-        if (k > 0 && !mbar_wait(s_free, static_cast<uint32_t>(k - 1) & 1u, abort_flag)) break;
-        const int s = k % C::ST;
-        if (!mbar_wait(&kfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) break;
-        tc_fence_after();
+    if (is_v) {
+      // ---------------------------------------------------------- V, O += P V
+      for (int item = 0; ok; ++item) {
+        const int keys = walk.q.L + walk.q.T;
+        // every row of the tile sees the keys before `open`; from there on rows differ
+        const int open = masked ? walk.q.L : walk.q.L + walk.tile * a.TT + 1;
+        bool taken_out = false;
+        for (int i = 0; i < walk.n; ++i, ++k) {
+          const int s = k % C::ST;
+          if (!warp_wait(&full[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const int kb = (walk.b0 + i) * kBlock;
+          if (kb + kBlock > open) {
+            // rows behind the last token to zero; elements that are not finite out of
+            // the rows that not every query sees
+            const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
+            uint8_t* v = ring + s * C::kKVBytes;
+            for (int c = 0; c < C::kChunks; ++c) {
+              for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
+                uint4* at = reinterpret_cast<uint4*>(v + c * C::kKVChunkBytes + x * 16);
+                if (x >= live * 8) {
+                  *at = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  uint4 w = *at;
+                  uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+                  bool any = false;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk & 3) * 32;
-          const uint64_t ad = sdesc_sw128(sQa + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
-          const uint64_t bd = sdesc_sw128(sKa + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
-          tc_mma_ss(tmem_base + C::kColS, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(s_full);
-        tc_commit(&kempty[s]);
-      }
-      tc_commit(drain);
-      mbar_wait_drain(drain, 0u);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ P.V issuer
-    const uint32_t sVa = smem_u32(sV);
-    bool taken_out = false;
-    for (int k = 0; k < n; ++k) {
-      const int s = k % C::ST;
-      if (!warp_wait(&vfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) break;
-      const int kb = (b0 + k) * kBlock;
-      if (kb + kBlock > open || kb + kBlock > keys) {
-        // rows behind the last token to zero; elements that are not finite out of
-        // the rows that not every query sees
-        const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
-        uint8_t* v = sV + s * C::kKVBytes;
-        for (int c = 0; c < C::kChunks; ++c) {
-          for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
-            uint4* at = reinterpret_cast<uint4*>(v + c * C::kKVChunkBytes + x * 16);
-            if (x >= live * 8) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint4 w = *at;
-              uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-              bool any = false;
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const bool lo = not_finite16<kElem>(e[u]), hi = not_finite16<kElem>(e[u] >> 16);
-                if (lo) e[u] &= 0xffff0000u;
-                if (hi) e[u] &= 0x0000ffffu;
-                any |= lo | hi;
-              }
-              if (any) {
-                *at = w;
-                taken_out = true;
+                  for (int u = 0; u < 4; ++u) {
+                    const bool lo = not_finite16<kElem>(e[u]), hi = not_finite16<kElem>(e[u] >> 16);
+                    if (lo) e[u] &= 0xffff0000u;
+                    if (hi) e[u] &= 0x0000ffffu;
+                    any |= lo | hi;
+                  }
+                  if (any) {
+                    *at = w;
+                    taken_out = true;
+                  }
+                }
               }
             }
+            fence_proxy_async_smem();
+            if (__any_sync(FULL, taken_out) && lane == 0) special[item & 1] = item + 1;
+            __syncwarp();
+          }
+          if (!warp_wait(&p_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t aP = tmem_base + ((k & 1) ? C::kColP1 : C::kColP0);
+#pragma unroll
+            for (int kk = 0; kk < kBlock / 16; ++kk) {
+              const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
+              tc_mma_ts(tmem_base + C::kColO, aP + kk * 8, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
+            }
+            tc_commit(&pv_done[k & 1]);
+            tc_commit(&empty[s]);
+            mbar_arrive(&pv_done[k & 1]);       // releases `special`
+          }
+          __syncwarp();
+          if (ld.more) {
+            if (!warp_wait(&empty[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            load_next();
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
+        if (!ok || !walk.next(a)) break;
       }
-      if (!warp_wait(&p_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t aP = tmem_base + ((k & 1) ? C::kColP1 : C::kColP0);
+    } else {
+      // ---------------------------------------------------------- Q, K, S = Q K^T
+      const uint32_t sQa = smem_u32(sQ);
+      TreeWalk qw = walk;                       // the tile whose Q is loaded next
+      bool q_more = true;
+      int q_issued = 0;
+      auto load_q = [&]() {
+        const int buf = q_issued % C::kQBufs;
+        if (lane == 0) {
+          const int tok = a.starts[qw.r] + qw.tile * a.TT;
+          mbar_expect_tx(&q_full[buf], C::kChunks * a.TT * a.G * 128);
 #pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk) {
-          const uint64_t bd = sdesc_sw128(sVa + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
-          tc_mma_ts(tmem_base + C::kColO, aP + kk * 8, bd, kIdescPV, (k > 0 || kk > 0) ? 1u : 0u);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(sQ + buf * C::kQBytes + c * C::kQChunkBytes, &tmQ, 0, qw.head * a.G, tok, c, &q_full[buf]);
         }
-        tc_commit(&pv_done[k & 1]);
-        tc_commit(&vempty[s]);
+        __syncwarp();
+        ++q_issued;
+        q_more = qw.next(a);
+      };
+      for (int b = 0; b < C::kQBufs && q_more; ++b) load_q();
+      for (int item = 0; ok; ++item) {
+        const int buf = item % C::kQBufs;
+        if (!warp_wait(&q_full[buf], static_cast<uint32_t>(item / C::kQBufs) & 1u, abort_flag)) break;
+        for (int i = 0; i < walk.n; ++i, ++k) {
+          const int s = k % C::ST;
+          if ((k > 0 && !warp_wait(s_free, static_cast<uint32_t>(k - 1) & 1u, abort_flag)) ||
+              !warp_wait(&full[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk & 3) * 32;
+              const uint64_t ad =
+                  sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
+              const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
+              tc_mma_ss(tmem_base + C::kColS, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(s_full);
+            tc_commit(&empty[s]);
+          }
+          __syncwarp();
+          // the stage, and after a tile's last block its Q, may be overwritten
+          if (!warp_wait(&empty[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (ld.more) load_next();
+        }
+        if (!ok) break;
+        if (q_more) load_q();
+        if (!walk.next(a)) break;
       }
-      __syncwarp();
+      for (int b = max(0, q_issued - C::kQBufs); b < q_issued; ++b)   // (bounded; complete unless aborted)
+        if (lane == 0) mbar_wait_drain(&q_full[b % C::kQBufs], static_cast<uint32_t>(b / C::kQBufs) & 1u);
     }
-    if (__any_sync(FULL, taken_out) && lane == 0) *special = 1;
+    if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
+    // every load and product that was issued has finished before the CTA leaves (bounded)
     if (lane == 0) {
-      mbar_arrive(drain);              // `special` is written
       tc_commit(drain);
       mbar_wait_drain(drain, 0u);
+      for (int b = max(0, issued - C::ST); b < issued; ++b)
+        mbar_wait_drain(&full[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
     }
   } else {
     // ------------------------------------------------------------ softmax warps
     const int wq = warp & 3;                       // TMEM lane quadrant: rows 32*wq ..
-    if (wq < nact) {
-      const int row = wq * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t s_addr = tmem_base + lane_bits + C::kColS;
+    const uint32_t o_addr = tmem_base + lane_bits + C::kColO;
+    const int row = wq * 32 + lane;
+    const int row_t = row / a.G, row_g = row - row_t * a.G;   // token of the tile, head of the group
+    bool alive = true;
+    int k = 0;                                     // blocks of the share
+    for (int item = 0; alive; ++item) {
+      const int t0 = walk.tile * a.TT;
+      const int rows = min(a.TT, walk.q.T - t0) * a.G;        // rows of the tile that exist
+      if (wq * 32 >= rows) {
+        for (int i = 0; i < walk.n; ++i, ++k) {
+          if (!warp_wait(s_full, static_cast<uint32_t>(k) & 1u, abort_flag)) {
+            alive = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive(s_free);
+            mbar_arrive(&p_full[k & 1]);
+          }
+        }
+        if (!alive || !walk.next(a)) break;
+        continue;
+      }
       const bool valid = row < rows;
-      const int tl = valid ? row / a.G : 0;         // token of the tile, head of the group
-      const int g = valid ? row - tl * a.G : 0;
-      const int t = t0 + tl;
-      const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
-      const uint32_t s_addr = tmem_base + lane_bits + C::kColS;
-      const uint32_t o_addr = tmem_base + lane_bits + C::kColO;
+      const int t = t0 + row_t;
+      const long long token = static_cast<long long>(a.starts[walk.r]) + t;
+      const int open = masked ? walk.q.L : walk.q.L + t0 + 1;
       float m_ref = -INFINITY, l = 0.f;
-      bool alive = true;
       float s[64];
-      if (warp_wait(s_full, 0u, abort_flag)) {
+      if (warp_wait(s_full, static_cast<uint32_t>(k) & 1u, abort_flag)) {
         tc_fence_after();
         tmem_ld32(s_addr, *reinterpret_cast<float(*)[32]>(&s[0]));
         tmem_ld32(s_addr + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
       } else {
         alive = false;
       }
-      for (int k = 0; alive && k < n; ++k) {
-        const int kb = (b0 + k) * kBlock;
+      for (int i = 0; alive && i < walk.n; ++i, ++k) {
+        const int kb = (walk.b0 + i) * kBlock;
         unsigned long long vis = ~0ull;
         const bool part = kb + kBlock > open;       // some row does not see the whole block
-        if (part) vis = valid ? tree_visible(a, rq.L, rq.T, t, tok0 + tl, kb) : 0ull;
+        if (part) vis = valid ? tree_visible(a, walk.q.L, walk.q.T, t, token, kb) : 0ull;
         tmem_wait_ld();
         pin32(*reinterpret_cast<float(*)[32]>(&s[0]));
         pin32(*reinterpret_cast<float(*)[32]>(&s[32]));
@@ -591,7 +765,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           tc_fence_after();
         }
         tmem_st32u(tmem_base + lane_bits + ((k & 1) ? C::kColP1 : C::kColP0), pk);
-        if (k > 0 && any_raise) {
+        if (i > 0 && any_raise) {
           if (!warp_wait(&pv_done[(k - 1) & 1], static_cast<uint32_t>((k - 1) >> 1) & 1u, abort_flag)) {
             alive = false;
             break;
@@ -608,7 +782,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             tmem_st32(o_addr + cc, o);
           }
         }
-        if (k + 1 < n) {
+        if (i + 1 < walk.n) {
           if (!warp_wait(s_full, static_cast<uint32_t>(k + 1) & 1u, abort_flag)) {
             alive = false;
             break;
@@ -623,38 +797,38 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (lane == 0) mbar_arrive(&p_full[k & 1]);
       }
       tmem_wait_ld();
-      // ------------------------------------------------------------ epilogue
-      if (alive && warp_wait(drain, 0u, abort_flag)) {
-        tc_fence_after();
-        const bool whole_row = pieces == 1;
-        const float mul = whole_row ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // a NaN sum stays one
-        const bool fix = *special != 0;
-        const long long token = tok0 + tl;
-        const int hq = head * a.G + g;
-        const long long prow = (static_cast<long long>(found[3]) + found[1]) * (a.TT * a.G) + row;
-        uint16_t* orow = static_cast<uint16_t*>(a.O) + token * a.o_token + hq * a.o_head;
+      // ------------------------------------------------------------ epilogue of the tile
+      if (!alive || !warp_wait(&pv_done[(k - 1) & 1], static_cast<uint32_t>((k - 1) >> 1) & 1u, abort_flag)) break;
+      tc_fence_after();
+      const bool whole_row = walk.b0 == 0 && walk.n == walk.nbt;
+      const float mul = whole_row ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // a NaN sum stays one
+      const bool fix = special[item & 1] == item + 1;
+      const int hq = walk.head * a.G + row_g;
+      const long long prow = (2LL * cta + (walk.b0 == 0 ? 1 : 0)) * (a.TT * a.G) + row;
+      uint16_t* orow = static_cast<uint16_t*>(a.O) + token * a.o_token + hq * a.o_head;
 #pragma unroll 1
-        for (int cc = 0; cc < D; cc += 32) {
-          float o[32];
-          tmem_ld32(o_addr + cc, o);
-          tmem_wait_ld();
-          pin32(o);
-          if (!valid) continue;
+      for (int cc = 0; cc < D; cc += 32) {
+        float o[32];
+        tmem_ld32(o_addr + cc, o);
+        tmem_wait_ld();
+        pin32(o);
+        if (valid) {
           if (l == 0.f) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = 0.f;
           }
           if (fix) {
             // the elements taken out of V, for the rows that see their token
-            for (int kb = b0 * kBlock; kb < b1 * kBlock; kb += kBlock) {
+            const int* trow = a.table + static_cast<long long>(walk.r) * a.width;
+            for (int kb = walk.b0 * kBlock; kb < (walk.b0 + walk.n) * kBlock; kb += kBlock) {
               if (kb + kBlock <= open) continue;
-              unsigned long long vis = tree_visible(a, rq.L, rq.T, t, token, kb);
+              unsigned long long vis = tree_visible(a, walk.q.L, walk.q.T, t, token, kb);
               if (open > kb) vis &= ~low_bits64(open - kb);
               for (; vis; vis &= vis - 1) {
                 const int at = kb + __ffsll(static_cast<long long>(vis)) - 1;
                 const int id = trow[at >> a.page_shift];
                 if (id < 0 || id >= a.pages) continue;
-                const uint16_t* v = Vraw + id * v_page + (at & (page - 1)) * v_token + head * v_head + cc;
+                const uint16_t* v = Vraw + id * v_page + (at & (page - 1)) * v_token + walk.head * v_head + cc;
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
                   const uint32_t e = v[x];
@@ -679,13 +853,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
         }
-        if (valid) {
-          if (!whole_row)
-            a.part_ml[prow] = make_float2(m_ref, l);
-          else if (a.lse)
-            a.lse[token * (a.Hkv * a.G) + hq] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
-        }
       }
+      if (valid) {
+        if (!whole_row)
+          a.part_ml[prow] = make_float2(m_ref, l);
+        else if (a.lse)
+          a.lse[token * (a.Hkv * a.G) + hq] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
+      }
+      tc_fence_before();                            // O is read before the next tile's P is published
+      if (!walk.next(a)) break;
     }
   }
   tc_fence_before();
@@ -696,8 +872,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
 }
 
-// Joins the pieces of the tiles that have more than one: for each row the largest of
-// the pieces' maxima, then O = sum w_p O_p / sum w_p l_p, w_p = 2^(m_p - m). One warp
+// Joins the pieces of the tiles that the shares' borders cut: for each row the largest
+// of the pieces' maxima, then O = sum w_p O_p / sum w_p l_p, w_p = 2^(m_p - m). One warp
 // for each (token, query head), pieces in ascending order.
 template <int D, int kElem>
 __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
@@ -715,33 +891,32 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
     else
       hi = mid;
   }
-  const int2 sc = a.sched[lo];
-  const int pieces = sc.x;
-  if (pieces <= 1) return;
-  bool bad = false;
+  bool bad;
+  const bool masked = a.mask != nullptr;
   const TreeReq q = tree_request(a, lo, &bad);
   const int t = token - a.starts[lo];
   if (t < 0 || t >= q.T) return;
   const int tile = t / a.TT, head = hq / a.G;
   const int row = (t - tile * a.TT) * a.G + (hq - head * a.G);
-  const int nbt = tree_tile_blocks(q, tile, a.TT, a.mask != nullptr);
-  // pieces that hold a block of this tile: those that start before its last one
-  int np = pieces;
-  while (np > 1 && tree_piece_start(q.nb, np - 1, pieces) >= nbt) --np;
+  const long long total = a.line[a.R];
+  const int ctas = static_cast<int>(a.line[a.R + 1]);
+  const long long first = a.line[lo] + head * tree_blocks_before(q, q.tiles, a.TT, masked) +
+                          tree_blocks_before(q, tile, a.TT, masked);
+  const int c0 = tree_owner(total, first, ctas);
+  const int c1 = tree_owner(total, first + tree_tile_blocks(q, tile, a.TT, masked) - 1, ctas);
+  if (c0 == c1) return;                             // one CTA had the whole tile and wrote it
   const int rows = a.TT * a.G;
-  const int rtile = q.tiles - 1 - tile;
-  const long long slot0 = sc.y + static_cast<long long>(head) * pieces * q.tiles + rtile;
-  auto prow = [&](int p) { return (slot0 + static_cast<long long>(p) * q.tiles) * rows + row; };
+  auto prow = [&](int c) { return (2LL * c + (c == c0 ? 1 : 0)) * rows + row; };
   float m = -INFINITY;
-  for (int p = lane; p < np; p += 32) m = fmaxf(m, a.part_ml[prow(p)].x);
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[prow(c)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float mref = m == -INFINITY ? 0.f : m;
   constexpr int kPer = D / 32;                      // elements of a lane
   float acc[kPer] = {}, l = 0.f;
 #pragma unroll 4
-  for (int p = 0; p < np; ++p) {
-    const long long at = prow(p);
+  for (int c = c0; c <= c1; ++c) {
+    const long long at = prow(c);
     const float2 ml = a.part_ml[at];
     const float w = ex2(ml.x - mref);
     float v[kPer];
