@@ -32,15 +32,18 @@
 // K and issues S = Q K^T, warps 2..5 run the softmax (thread = row), the O correction
 // and the epilogue; a softmax warp whose 32 rows do not exist only keeps the barriers'
 // counts, so a single-token call pays the exponentials of one warp. TMEM (256 columns):
-// S [0,64), P [64,96) and [96,128), O [128, 128 + D). Two CTAs fit on an SM.
+// S(k) in [0,64) or [64,128) by k's parity, P(k) over its first half, O [128, 128 + D).
+// Two CTAs fit on an SM.
 //
 // Blocks are counted through the CTA's whole share, tiles included, and so are the
-// barrier phases: block k uses ring stage k % ST, S and P as in the block-sparse forward:
-// S(k+1) is issued only after every softmax warp released S(k); P(k) goes to buffer
-// k & 1 once P(k-2).V has finished; a stage is refilled after the product that read it
-// has completed. A tile's first P.V overwrites O: its P is published only after the
-// softmax warps have read the tile before out of TMEM. So no wait is ever more than one
-// phase behind its barrier.
+// barrier phases: block k uses ring stage k % ST. S(k+2) is issued once P(k).V has
+// finished, which needs P(k) of every softmax warp, so each has read S(k) and waited for
+// it; the softmax of k+1 runs meanwhile on an S that was there when it began. P(k) goes
+// over S(k): a warp stores its own rows after it has loaded them. A stage is refilled
+// after the product that read it has completed. A tile's first P.V overwrites O: its P
+// is published only after the softmax warps have read the tile before out of TMEM. The
+// softmax waits for P(k-1).V only to correct O. So no wait is ever more than one phase
+// behind its barrier.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -92,7 +95,7 @@ struct TreeCfg {
   static constexpr int kNumBars = 4 * ST + kQBufs + 7;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int kSmemBytes = oMisc + 512;
-  static constexpr uint32_t kColS = 0, kColP0 = 64, kColP1 = 96, kColO = 128, kTmemCols = 256;
+  static constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;   // S(k), then P(k): kColS + 64 (k & 1)
   static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs on an SM");
 };
 
@@ -230,6 +233,24 @@ __device__ __forceinline__ float to_float16(uint32_t bits) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
 }
 
+// p = 2^(s * sc - nm) for 32 columns of a row: P as 16-bit pairs, the sums of the p on
+// two pairs of accumulators.
+template <int kElem>
+__device__ __forceinline__ void tree_exp32(const float (&s)[32], uint64_t sc2, uint64_t nm2, uint64_t& acc0,
+                                           uint64_t& acc1, uint32_t* pk) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    float x0, x1;
+    f2unpack(ffma2(f2pack(s[c], s[c + 1]), sc2, nm2), x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    if ((c >> 1) & 1)
+      acc1 = fadd2(acc1, f2pack(p0, p1));
+    else
+      acc0 = fadd2(acc0, f2pack(p0, p1));
+    pk[c >> 1] = pack16x2<kElem>(p0, p1);
+  }
+}
+
 // A walk along a CTA's share of the line, tile by tile: the piece of the current tile
 // is its blocks [b0, b0 + n). A piece that begins inside its tile is kept for the end, so
 // that every CTA begins with block 0 of some tile: the CTAs on one key head then read the
@@ -349,8 +370,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   uint64_t* vfull = kempty + C::ST;        // [ST] V stage loaded
   uint64_t* vempty = vfull + C::ST;        // [ST] V stage consumed by P.V MMA
   uint64_t* q_full = vempty + C::ST;       // [kQBufs] Q of a tile loaded
-  uint64_t* s_full = q_full + C::kQBufs;   // S(k) written by the MMA (phase k)
-  uint64_t* s_free = s_full + 1;           // S(k) read by the softmax warps (phase k)
+  uint64_t* s_full = q_full + C::kQBufs;   // [2] by k parity: S(k) written by the MMA
   uint64_t* p_full = s_full + 2;           // [2] by k parity: P(k) in TMEM and O corrected
   uint64_t* pv_done = s_full + 4;          // [2] by k parity: P(k).V finished (the MMA and `special`)
   uint64_t* drain = s_full + 6;            // every MMA of the CTA finished
@@ -374,8 +394,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(&vempty[s], 1);
     }
     for (int b = 0; b < C::kQBufs; ++b) mbar_init(&q_full[b], 1);
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
     mbar_init(&p_full[0], 4);
     mbar_init(&p_full[1], 4);
     mbar_init(&pv_done[0], 2);
@@ -570,7 +590,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           }
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t aP = tmem_base + ((k & 1) ? C::kColP1 : C::kColP0);
+            const uint32_t aP = tmem_base + C::kColS + (k & 1) * 64;
 #pragma unroll
             for (int kk = 0; kk < kBlock / 16; ++kk) {
               const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
@@ -616,7 +636,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (!warp_wait(&q_full[buf], static_cast<uint32_t>(item / C::kQBufs) & 1u, abort_flag)) break;
         for (int i = 0; i < walk.n; ++i, ++k) {
           const int s = k % C::ST;
-          if ((k > 0 && !warp_wait(s_free, static_cast<uint32_t>(k - 1) & 1u, abort_flag)) ||
+          if ((k > 1 && !warp_wait(&pv_done[k & 1], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag)) ||
               !warp_wait(&full[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
             ok = false;
             break;
@@ -629,9 +649,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               const uint64_t ad =
                   sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
               const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
-              tc_mma_ss(tmem_base + C::kColS, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+              tc_mma_ss(tmem_base + C::kColS + (k & 1) * 64, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
             }
-            tc_commit(s_full);
+            tc_commit(&s_full[k & 1]);
             tc_commit(&empty[s]);
           }
           __syncwarp();
@@ -672,14 +692,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const int rows = min(a.TT, walk.q.T - t0) * a.G;        // rows of the tile that exist
       if (wq * 32 >= rows) {
         for (int i = 0; i < walk.n; ++i, ++k) {
-          if (!warp_wait(s_full, static_cast<uint32_t>(k) & 1u, abort_flag)) {
+          if (!warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
             alive = false;
             break;
           }
-          if (lane == 0) {
-            mbar_arrive(s_free);
-            mbar_arrive(&p_full[k & 1]);
-          }
+          if (lane == 0) mbar_arrive(&p_full[k & 1]);
         }
         if (!alive || !walk.next(a)) break;
         continue;
@@ -689,11 +706,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const long long token = static_cast<long long>(a.starts[walk.r]) + t;
       const int open = masked ? walk.q.L : walk.q.L + t0 + 1;
       float m_ref = -INFINITY, l = 0.f;
-      float s[64];
-      if (warp_wait(s_full, static_cast<uint32_t>(k) & 1u, abort_flag)) {
+      float s0[32], s1[32];                        // S(k) of the row: columns 0..31 and 32..63
+      if (warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
         tc_fence_after();
-        tmem_ld32(s_addr, *reinterpret_cast<float(*)[32]>(&s[0]));
-        tmem_ld32(s_addr + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
+        tmem_ld32(s_addr + (k & 1) * 64, s0);
+        tmem_ld32(s_addr + (k & 1) * 64 + 32, s1);
       } else {
         alive = false;
       }
@@ -703,29 +720,25 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         const bool part = kb + kBlock > open;       // some row does not see the whole block
         if (part) vis = valid ? tree_visible(a, walk.q.L, walk.q.T, t, token, kb) : 0ull;
         tmem_wait_ld();
-        pin32(*reinterpret_cast<float(*)[32]>(&s[0]));
-        pin32(*reinterpret_cast<float(*)[32]>(&s[32]));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
+        pin32(s0);
+        pin32(s1);
         if (part) {
           const uint32_t vlo = static_cast<uint32_t>(vis), vhi = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            s[c] = (vlo >> c) & 1u ? s[c] : -INFINITY;
-            s[c + 32] = (vhi >> c) & 1u ? s[c + 32] : -INFINITY;
+            s0[c] = (vlo >> c) & 1u ? s0[c] : -INFINITY;
+            s1[c] = (vhi >> c) & 1u ? s1[c] : -INFINITY;
           }
         }
         float mx[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) mx[u] = fmax3(s[u], s[u + 8], s[u + 16]);
+        for (int u = 0; u < 8; ++u) mx[u] = fmax3(s0[u], s0[u + 8], s0[u + 16]);
 #pragma unroll
-        for (int c = 24; c < 56; c += 16) {
+        for (int u = 0; u < 8; ++u) mx[u] = fmax3(mx[u], s0[u + 24], s1[u]);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) mx[u] = fmax3(mx[u], s[c + u], s[c + 8 + u]);
-        }
+        for (int u = 0; u < 8; ++u) mx[u] = fmax3(mx[u], s1[u + 8], s1[u + 16]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], s[56 + u]);
+        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], s1[u + 24]);
         const float rmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
                            a.scale_log2;
         // the reference maximum is raised only when a row's maximum grows by more
@@ -741,30 +754,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         uint32_t pk[32];
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
         const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2), nm2 = f2pack(-mref, -mref);
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float x0, x1;
-          f2unpack(ffma2(f2pack(s[c], s[c + 1]), sc2, nm2), x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          if ((c >> 1) & 1)
-            acc1 = fadd2(acc1, f2pack(p0, p1));
-          else
-            acc0 = fadd2(acc0, f2pack(p0, p1));
-          pk[c >> 1] = pack16x2<kElem>(p0, p1);
-        }
+        tree_exp32<kElem>(s0, sc2, nm2, acc0, acc1, pk);
+        tree_exp32<kElem>(s1, sc2, nm2, acc0, acc1, pk + 16);
+        tmem_st32u(s_addr + (k & 1) * 64, pk);
         float r0, r1, r2, r3;
         f2unpack(acc0, r0, r1);
         f2unpack(acc1, r2, r3);
         l = l * alpha + ((r0 + r1) + (r2 + r3));
-        // P(k) into buffer k & 1 once its previous reader, P(k-2).V, has finished
-        if (k >= 2) {
-          if (!warp_wait(&pv_done[k & 1], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag)) {
-            alive = false;
-            break;
-          }
-          tc_fence_after();
-        }
-        tmem_st32u(tmem_base + lane_bits + ((k & 1) ? C::kColP1 : C::kColP0), pk);
         if (i > 0 && any_raise) {
           if (!warp_wait(&pv_done[(k - 1) & 1], static_cast<uint32_t>((k - 1) >> 1) & 1u, abort_flag)) {
             alive = false;
@@ -782,19 +778,19 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             tmem_st32(o_addr + cc, o);
           }
         }
-        if (i + 1 < walk.n) {
-          if (!warp_wait(s_full, static_cast<uint32_t>(k + 1) & 1u, abort_flag)) {
-            alive = false;
-            break;
-          }
-          tc_fence_after();
-          tmem_ld32(s_addr, *reinterpret_cast<float(*)[32]>(&s[0]));
-          tmem_ld32(s_addr + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
-        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[k & 1]);
+        if (i + 1 < walk.n) {
+          if (!warp_wait(&s_full[(k + 1) & 1], static_cast<uint32_t>((k + 1) >> 1) & 1u, abort_flag)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          tmem_ld32(s_addr + ((k + 1) & 1) * 64, s0);
+          tmem_ld32(s_addr + ((k + 1) & 1) * 64 + 32, s1);
+        }
       }
       tmem_wait_ld();
       // ------------------------------------------------------------ epilogue of the tile
