@@ -18,7 +18,6 @@
 namespace {
 
 constexpr int kSMs = 148;                       // B200
-constexpr int kTreeCtas = 2 * kSMs;             // two CTAs on every SM share the call's key blocks
 constexpr int kTreeMinBlocks = 2;               // smallest share of a CTA, in 64-key blocks
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -110,7 +109,8 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, const sa_cache& c) {
 
 // The tiling and workspace of sparse_attn_tree_fwd, from what the host knows.
 struct TreeLayout {
-  int G, TT;
+  int G, TC, chains;          // query heads of a key head, tokens of a chain, chains of a CTA
+  int ctas;                   // CTAs that share the call's key blocks
   bool split;                 // the border between two CTAs' shares may cut a tile
   size_t part_o, part_ml, line, total;
 };
@@ -118,10 +118,12 @@ TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   TreeLayout L{};
   L.G = Hq / c.Hkv;
-  L.TT = 128 / L.G;
-  L.TT = std::min(L.TT, s.max_new > 0 ? std::min(s.max_new, s.n) : s.n);
+  const int most = s.max_new > 0 ? std::min(s.max_new, s.n) : s.n;   // new tokens of a request
+  L.TC = std::min(128 / L.G, most);
+  L.chains = most > L.TC ? 2 : 1;
+  L.ctas = L.chains == 2 ? kSMs : 2 * kSMs;
   L.split = static_cast<int64_t>(s.width) * c.page_size > sa::kBlock;
-  const size_t rows = L.split ? size_t{2} * kTreeCtas * L.TT * L.G : 0;
+  const size_t rows = L.split ? size_t{2} * L.ctas * L.chains * L.TC * L.G : 0;
   size_t o = 0;
   L.part_o = o; o += al(rows * c.d * sizeof(float));
   L.part_ml = o; o += al(rows * sizeof(float2));
@@ -130,16 +132,16 @@ TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
   return L;
 }
 
-template <int D, int kElem, bool kSmallQ>
+template <int D, int kElem, int NC, bool kSmallQ>
 sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const sa::TreeArgs& a,
-                      const void* V, const sa_cache& c, bool split, cudaStream_t st) {
-  using Cfg = sa::TreeCfg<D, kSmallQ>;
-  auto kern = sa::tree_fwd_kernel<D, kElem, kSmallQ>;
+                      const void* V, const sa_cache& c, const TreeLayout& L, cudaStream_t st) {
+  using Cfg = sa::TreeCfg<D, NC, kSmallQ>;
+  auto kern = sa::tree_fwd_kernel<D, kElem, NC, kSmallQ>;
   if (sa::set_smem(kern, Cfg::kSmemBytes) != SA_OK) return SA_ERR_CUDA;
-  kern<<<kTreeCtas, sa::kTreeThreads, Cfg::kSmemBytes, st>>>(mq, mk, mv, a, static_cast<const uint16_t*>(V),
-                                                        c.page_stride, c.token_stride, c.head_stride);
+  kern<<<L.ctas, Cfg::kThreads, Cfg::kSmemBytes, st>>>(mq, mk, mv, a, static_cast<const uint16_t*>(V), c.page_stride,
+                                                       c.token_stride, c.head_stride);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
-  if (split) {
+  if (L.split) {
     const int64_t warps = static_cast<int64_t>(a.n) * a.Hkv * a.G;
     sa::tree_combine_kernel<D, kElem><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
@@ -282,7 +284,7 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   const TreeLayout L = tree_layout(c, s, Hq);
   if (L.total > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total)) return SA_ERR_WORKSPACE;
   CUtensorMap mq, mk, mv;
-  if (!make_q_map(&mq, Q, q_token, q_head, s.n, Hq, c.d, L.G, L.TT) || !make_cache_map(&mk, K_cache, c) ||
+  if (!make_q_map(&mq, Q, q_token, q_head, s.n, Hq, c.d, L.G, L.TC) || !make_cache_map(&mk, K_cache, c) ||
       !make_cache_map(&mv, V_cache, c))
     return SA_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
@@ -300,7 +302,8 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   a.words = s.words;
   a.Hkv = c.Hkv;
   a.G = L.G;
-  a.TT = L.TT;
+  a.TT = L.chains * L.TC;
+  a.TC = L.TC;
   a.min_blocks = kTreeMinBlocks;
   a.O = O;
   a.o_token = s.n > 1 ? o_token : 0;
@@ -313,10 +316,11 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
     a.line = reinterpret_cast<long long*>(ws + L.line);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool small = L.TT * L.G <= 32, f16 = c.dtype == SA_F16;
-#define SA_TREE(D, E)                                                                      \
-  (small ? launch_tree<D, E, true>(mq, mk, mv, a, V_cache, c, L.split, st)           \
-         : launch_tree<D, E, false>(mq, mk, mv, a, V_cache, c, L.split, st))
+  const bool small = L.TC * L.G <= 32, f16 = c.dtype == SA_F16;
+#define SA_TREE(D, E)                                                                \
+  (L.chains == 2 ? launch_tree<D, E, 2, false>(mq, mk, mv, a, V_cache, c, L, st)     \
+   : small       ? launch_tree<D, E, 1, true>(mq, mk, mv, a, V_cache, c, L, st)      \
+                 : launch_tree<D, E, 1, false>(mq, mk, mv, a, V_cache, c, L, st))
   if (c.d == 64) return f16 ? SA_TREE(64, sa::kElemF16) : SA_TREE(64, sa::kElemBF16);
   return f16 ? SA_TREE(128, sa::kElemF16) : SA_TREE(128, sa::kElemBF16);
 #undef SA_TREE

@@ -52,8 +52,6 @@
 
 namespace sa {
 
-constexpr int kTreeThreads = 192;
-
 // 16-bit element types of Q, K, V, P and O.
 enum Elem16 : int { kElemBF16 = 0, kElemF16 = 1 };
 
@@ -74,42 +72,52 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   }
 }
 
+// NC: chains of a CTA, 128 rows each. Two chains (one CTA on an SM) read every K and V
+// block once for 256 rows; a tile of at most 128 rows has one chain, two CTAs on an SM.
 // kSmallQ: the tile has at most 32 rows, so Q takes 32 rows of shared memory (twice, so
 // that the next tile's is there early) and the freed space a third stage of K and of V.
 // The S product still reads 128 rows (rows behind Q are whatever lies there); a row's
 // result touches no other row, and the rows that do not exist are never written out.
-template <int D, bool kSmallQ>
+template <int D, int NC, bool kSmallQ>
 struct TreeCfg {
+  static_assert(!(kSmallQ && NC > 1), "a small tile is one chain");
+  static constexpr int kThreads = 192 * NC;         // 2 issue and 4 softmax warps for each chain
+  static constexpr int kCtas = NC == 1 ? 2 : 1;            // on an SM
   static constexpr int kChunks = D / 64;
   static constexpr int kQRows = kSmallQ ? 32 : 128;
   static constexpr int kQBufs = kSmallQ ? 2 : 1;
   static constexpr int kQChunkBytes = kQRows * 128;
-  static constexpr int kQBytes = kChunks * kQChunkBytes;
+  static constexpr int kQBytes = kChunks * kQChunkBytes;   // one chain's
   static constexpr int kKVChunkBytes = kBlock * 128;
   static constexpr int kKVBytes = kChunks * kKVChunkBytes;
-  static constexpr int ST = D == 64 ? (kSmallQ ? 6 : 5) : (kSmallQ ? 3 : 2);   // stages of K and of V
+  static constexpr int ST =                                // stages of K and of V
+      NC == 2 ? (D == 64 ? 10 : 5) : (D == 64 ? (kSmallQ ? 6 : 5) : (kSmallQ ? 3 : 2));
+  // a stage is refilled this many blocks after its product was issued: with two chains
+  // the other one's product of the block has to be done too
+  static constexpr int kLag = NC == 2 ? 2 : 0;
   static constexpr int oQ = 0;
-  static constexpr int oK = oQ + kQBufs * kQBytes;
+  static constexpr int oK = oQ + NC * kQBufs * kQBytes;
   static constexpr int oV = oK + ST * kKVBytes;
   static constexpr int oBar = oV + ST * kKVBytes;
-  static constexpr int kNumBars = 4 * ST + kQBufs + 7;
+  static constexpr int kNumBars = 5 * ST + NC * (kQBufs + 6) + 1;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int kSmemBytes = oMisc + 512;
-  static constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;   // S(k), then P(k): kColS + 64 (k & 1)
-  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs on an SM");
+  static constexpr uint32_t kColS = 0, kColO = 128, kChainCols = 256;   // S(k), then P(k): kColS + 64 (k & 1)
+  static_assert(ST < 16, "the ring of `special`");
+  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 struct TreeArgs {
   const int *starts, *lens, *granted, *table;
   const uint32_t* mask;           // [n][words] or null
   int R, n, width, pages, page_shift, words;
-  int Hkv, G, TT;                 // key heads, query heads each, tokens of a tile
+  int Hkv, G, TT, TC;             // key heads, query heads each, tokens of a tile, of a chain's part of it
   int min_blocks;                 // smallest share of a CTA, in blocks
   void* O;
   long long o_token, o_head;      // strides in elements
   float* lse;                     // [n][Hkv * G] or null
   float scale_log2;
-  float* part_o;                  // [2 * CTA + (0: the piece ends its tile, or 1: begins it)][tile rows][D]
+  float* part_o;                  // [2 * CTA + (0: the piece ends its tile, or 1: begins it)][TT * G][D]
   float2* part_ml;                // [as part_o][tile rows]
   long long* line;                // [R + 2]: each request's first block on the line, the line's length, `ctas`
 };
@@ -312,49 +320,45 @@ struct TreeWalk {
   }
 };
 
-// A walk block by block, for the loads, with the lane's page of the current block
-// fetched one block ahead.
+// A walk block by block, for the loads. The lanes hold the ids of the 32 pages from `base`
+// on, and of the 32 behind them, read a window ahead of their use: a read of one id a
+// block cost its warp 700 cycles a block. (A block's pages never lie in two windows.)
 struct TreeLoad {
   TreeWalk w;
   int k;                          // block of the piece
   bool more;
-  int id;                         // this lane's page of it, -1: nothing to load
   const int* row;
-  __device__ __forceinline__ void fetch(const TreeArgs& a, bool loads, int off, bool* bad) {
-    id = -1;
-    if (!more) return;
-    const int at = (w.b0 + k) * kBlock + off;
-    if (!loads || at >= w.q.L + w.q.T) return;
-    id = row[at >> a.page_shift];
-    if (id < 0 || id >= a.pages) {
-      *bad = true;
-      id = 0;                     // flagged; any page of the pool keeps the load in bounds
-    }
-  }
-  __device__ __forceinline__ void begin(const TreeArgs& a, const TreeWalk& from) {
-    w = from;
+  int base, pages, ids, ahead;
+  __device__ __forceinline__ int read(int p) const { return p < pages ? row[p] : 0; }
+  __device__ __forceinline__ void open(const TreeArgs& a, int lane) {
     k = 0;
-    more = true;
     row = a.table + static_cast<long long>(w.r) * a.width;
+    pages = (w.q.L + w.q.T + (1 << a.page_shift) - 1) >> a.page_shift;
+    base = (w.b0 * kBlock) >> a.page_shift;
+    ids = read(base + lane);
+    ahead = read(base + 32 + lane);
   }
-  __device__ __forceinline__ void step(const TreeArgs& a) {
+  __device__ __forceinline__ void step(const TreeArgs& a, int lane) {
     if (++k == w.n) {
-      k = 0;
       more = w.next(a);
-      row = a.table + static_cast<long long>(w.r) * a.width;
+      if (more) open(a, lane);
+    } else if (((w.b0 + k) * kBlock >> a.page_shift) >= base + 32) {
+      base += 32;
+      ids = ahead;
+      ahead = read(base + 32 + lane);
     }
   }
 };
 
-template <int D, int kElem, bool kSmallQ>
-__global__ void __launch_bounds__(kTreeThreads, 2)
+template <int D, int kElem, int NC, bool kSmallQ>
+__global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, NC, kSmallQ>::kCtas)
     tree_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a,
                     const uint16_t* __restrict__ Vraw, long long v_page, long long v_token, long long v_head) {
-  using C = TreeCfg<D, kSmallQ>;
+  using C = TreeCfg<D, NC, kSmallQ>;
   constexpr uint32_t kIdescS = idesc_16_f32(kElem, 128, 64, false);
   constexpr uint32_t kIdescPV = idesc_16_f32(kElem, 128, D, true);
-  constexpr int kWarps = kTreeThreads / 32;
+  constexpr int kWarps = C::kThreads / 32;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* base = tree_smem;
   if (smem_u32(base) & 1023u) {               // the swizzled tiles need it; the kernel has no static shared memory
@@ -366,21 +370,22 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   uint8_t* sV = base + C::oV;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::oBar);
   uint64_t* kfull = bars;                  // [ST] K stage loaded
-  uint64_t* kempty = kfull + C::ST;        // [ST] K stage consumed by S MMA
+  uint64_t* kempty = kfull + C::ST;        // [ST] K stage consumed by every chain's S MMA
   uint64_t* vfull = kempty + C::ST;        // [ST] V stage loaded
-  uint64_t* vempty = vfull + C::ST;        // [ST] V stage consumed by P.V MMA
-  uint64_t* q_full = vempty + C::ST;       // [kQBufs] Q of a tile loaded
-  uint64_t* s_full = q_full + C::kQBufs;   // [2] by k parity: S(k) written by the MMA
-  uint64_t* p_full = s_full + 2;           // [2] by k parity: P(k) in TMEM and O corrected
-  uint64_t* pv_done = s_full + 4;          // [2] by k parity: P(k).V finished (the MMA and `special`)
-  uint64_t* drain = s_full + 6;            // every MMA of the CTA finished
+  uint64_t* vempty = vfull + C::ST;        // [ST] V stage consumed by every chain's P.V MMA
+  uint64_t* vready = vempty + C::ST;       // [ST] V stage loaded and its unseen rows dealt with (two chains)
+  uint64_t* q_full = vready + C::ST;       // [NC][kQBufs] Q of a tile loaded
+  uint64_t* s_full = q_full + NC * C::kQBufs;   // [NC][2] by block parity: S(k) written by the MMA
+  uint64_t* p_full = s_full + 2 * NC;      // [NC][2] by block parity: P(k) in TMEM and O corrected
+  uint64_t* pv_done = p_full + 2 * NC;     // [NC][2] by block parity: P(k).V finished (the MMA and `special`)
+  uint64_t* drain = pv_done + 2 * NC;      // every MMA of the CTA finished
   int* misc = reinterpret_cast<int*>(base + C::oMisc);
   volatile int* abort_flag = misc + 0;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 1);
-  volatile int* special = misc + 2;        // [2] by tile parity: 1 + a tile of which an element of V was taken out
-  int* found = misc + 4;                   // the share's first request, its T and L
-  long long* found_at = reinterpret_cast<long long*>(misc + 8);   // the request's first block on the line
-  long long* wsum = reinterpret_cast<long long*>(misc + 16);      // [kWarps]
+  int* found = misc + 2;                   // the share's first request, its T and L
+  volatile int* special = misc + 8;        // [16] by piece: 1 + a piece of which an element of V was taken out
+  long long* found_at = reinterpret_cast<long long*>(misc + 24);  // the request's first block on the line
+  long long* wsum = reinterpret_cast<long long*>(misc + 26);      // [kWarps]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned FULL = 0xffffffffu;
@@ -389,29 +394,28 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], NC);
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vempty[s], NC);
+      mbar_init(&vready[s], 1);
     }
-    for (int b = 0; b < C::kQBufs; ++b) mbar_init(&q_full[b], 1);
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(&p_full[0], 4);
-    mbar_init(&p_full[1], 4);
-    mbar_init(&pv_done[0], 2);
-    mbar_init(&pv_done[1], 2);
-    mbar_init(drain, 2);
+    for (int b = 0; b < NC * C::kQBufs; ++b) mbar_init(&q_full[b], 1);
+    for (int b = 0; b < 2 * NC; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], 4);
+      mbar_init(&pv_done[b], 2);
+    }
+    mbar_init(drain, 2 * NC);
     fence_mbar_init();
     *abort_flag = 0;
-    special[0] = 0;
-    special[1] = 0;
+    for (int b = 0; b < 16; ++b) special[b] = 0;
     found[0] = -1;
   }
   bool bad = false;
   const bool masked = a.mask != nullptr;
   TreeReq mine{0, 0, 0, 0};
   long long blocks = 0, total = 0;            // of the thread's request, of all
-  for (int r = threadIdx.x; r < a.R; r += kTreeThreads) {
+  for (int r = threadIdx.x; r < a.R; r += C::kThreads) {
     mine = tree_request(a, r, &bad);
     blocks = tree_blocks_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
     total += blocks;
@@ -435,9 +439,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   const long long share1 = ctas > 0 ? tree_share(total, cta + 1, ctas) : 0;
   __syncthreads();
   long long before = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kTreeThreads) {
+  for (int r0 = 0; r0 < a.R; r0 += C::kThreads) {
     const int r = r0 + threadIdx.x;
-    if (a.R > kTreeThreads) {
+    if (a.R > C::kThreads) {
       bool again;
       mine = r < a.R ? tree_request(a, r, &again) : TreeReq{0, 0, 0, 0};
       blocks = r < a.R ? tree_blocks_before(mine, mine.tiles, a.TT, masked) * a.Hkv : 0;
@@ -501,65 +505,86 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   const bool loads = subs == 1 ? lane == 0 : my_chunk < C::kChunks;
   const int sub_off = my_sub * sub, dst_off = my_chunk * C::kKVChunkBytes + sub_off * 128;
 
-  if (warp == 1) tmem_alloc(tmem_holder, C::kTmemCols);
+  if (warp == 0) tmem_alloc(tmem_holder, NC * C::kChainCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  if (warp < 2) {
-    // Both issue warps run the same ring: stage k % ST holds block k of the share, loaded
-    // when the product that read block k - ST has completed.
-    const bool is_v = warp == 0;
+  if (warp < 2 * NC) {
+    // Issue warps: 0 .. NC-1 the P V products, NC .. 2NC-1 the S products of a chain. Warp
+    // 0 loads V, warp NC loads K: stage k % ST holds block k of the share, refilled when the
+    // products that read block k - ST have completed.
+    const bool is_v = warp < NC;
+    const int c = is_v ? warp : warp - NC;
+    const bool loader = c == 0;
     uint8_t* ring = is_v ? sV : sK;
     uint64_t* full = is_v ? vfull : kfull;
     uint64_t* empty = is_v ? vempty : kempty;
     const CUtensorMap* map = is_v ? &tmV : &tmK;
-    if (lane == 0) tma_prefetch_desc(map);
     bool bad_page = false;
     TreeLoad ld;
-    ld.begin(a, walk);
-    ld.fetch(a, loads, sub_off, &bad_page);
+    ld.w = walk;
+    ld.more = loader;
     int issued = 0;
     auto load_next = [&]() {
       const int s = issued % C::ST;
-      const int kb = (ld.w.b0 + ld.k) * kBlock;
-      const int boxes = (min(ld.w.q.L + ld.w.q.T - kb, kBlock) + sub - 1) >> sub_shift;
+      const int at = (ld.w.b0 + ld.k) * kBlock + sub_off, keys = ld.w.q.L + ld.w.q.T;   // the lane's box
+      const int boxes = (min(keys - at + sub_off, kBlock) + sub - 1) >> sub_shift;
+      int id = __shfl_sync(FULL, ld.ids, (at >> a.page_shift) - ld.base);
       if (lane == 0) mbar_expect_tx(&full[s], static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks);
       __syncwarp();
-      if (ld.id >= 0)
-        tma_load_5d(ring + s * C::kKVBytes + dst_off, map, 0, (kb + sub_off) & (page - 1), my_chunk, ld.w.head, ld.id,
-                    &full[s]);
+      if (loads && at < keys) {
+        if (id < 0 || id >= a.pages) {
+          bad_page = true;
+          id = 0;                                 // flagged; any page of the pool keeps the load in bounds
+        }
+        tma_load_5d(ring + s * C::kKVBytes + dst_off, map, 0, at & (page - 1), my_chunk, ld.w.head, id, &full[s]);
+      }
       ++issued;
-      ld.step(a);
-      ld.fetch(a, loads, sub_off, &bad_page);
+      ld.step(a, lane);
     };
-    for (int s = 0; s < C::ST && ld.more; ++s) load_next();
+    if (loader) {
+      if (lane == 0) tma_prefetch_desc(map);
+      ld.open(a, lane);
+      for (int s = 0; s < C::ST && ld.more; ++s) load_next();
+    }
+    // after block k's product was issued: the stage of block k - kLag gets block k - kLag + ST
+    auto refill = [&](int k) {
+      if (!ld.more || k < C::kLag) return true;
+      const int b = k - C::kLag;
+      if (!warp_wait(&empty[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u, abort_flag)) return false;
+      load_next();
+      return true;
+    };
     const uint32_t ring_a = smem_u32(ring);
-    int k = 0;                                  // blocks of the share
+    const uint32_t tS = tmem_base + c * C::kChainCols + C::kColS, tO = tmem_base + c * C::kChainCols + C::kColO;
+    int k = 0, kc = 0;                            // blocks of the share, of the chain
     bool ok = true;
     if (is_v) {
-      // ---------------------------------------------------------- V, O += P V
-      for (int item = 0; ok; ++item) {
+      // ---------------------------------------------------------- O += P V
+      int item = 0;
+      do {
+        const bool act = walk.tile * a.TT + c * a.TC < walk.q.T;
         const int keys = walk.q.L + walk.q.T;
         // every row of the tile sees the keys before `open`; from there on rows differ
         const int open = masked ? walk.q.L : walk.q.L + walk.tile * a.TT + 1;
         bool taken_out = false;
         for (int i = 0; i < walk.n; ++i, ++k) {
           const int s = k % C::ST;
-          if (!warp_wait(&full[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+          if (!warp_wait(c == 0 ? &vfull[s] : &vready[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
             ok = false;
             break;
           }
           const int kb = (walk.b0 + i) * kBlock;
-          if (kb + kBlock > open) {
+          if (c == 0 && kb + kBlock > open) {
             // rows behind the last token to zero; elements that are not finite out of
             // the rows that not every query sees
             const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
             uint8_t* v = ring + s * C::kKVBytes;
-            for (int c = 0; c < C::kChunks; ++c) {
+            for (int h = 0; h < C::kChunks; ++h) {
               for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
-                uint4* at = reinterpret_cast<uint4*>(v + c * C::kKVChunkBytes + x * 16);
+                uint4* at = reinterpret_cast<uint4*>(v + h * C::kKVChunkBytes + x * 16);
                 if (x >= live * 8) {
                   *at = make_uint4(0u, 0u, 0u, 0u);
                 } else {
@@ -581,93 +606,110 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               }
             }
             fence_proxy_async_smem();
-            if (__any_sync(FULL, taken_out) && lane == 0) special[item & 1] = item + 1;
+            if (__any_sync(FULL, taken_out) && lane == 0) special[item & 15] = item + 1;
             __syncwarp();
           }
-          if (!warp_wait(&p_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t aP = tmem_base + C::kColS + (k & 1) * 64;
-#pragma unroll
-            for (int kk = 0; kk < kBlock / 16; ++kk) {
-              const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
-              tc_mma_ts(tmem_base + C::kColO, aP + kk * 8, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
-            }
-            tc_commit(&pv_done[k & 1]);
-            tc_commit(&empty[s]);
-            mbar_arrive(&pv_done[k & 1]);       // releases `special`
-          }
-          __syncwarp();
-          if (ld.more) {
-            if (!warp_wait(&empty[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+          if (NC > 1 && c == 0 && lane == 0) mbar_arrive(&vready[s]);
+          if (act) {
+            if (!warp_wait(&p_full[2 * c + (kc & 1)], static_cast<uint32_t>(kc >> 1) & 1u, abort_flag)) {
               ok = false;
               break;
             }
-            load_next();
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int kk = 0; kk < kBlock / 16; ++kk) {
+                const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
+                tc_mma_ts(tO, tS + (kc & 1) * 64 + kk * 8, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
+              }
+              tc_commit(&pv_done[2 * c + (kc & 1)]);
+              tc_commit(&vempty[s]);
+              mbar_arrive(&pv_done[2 * c + (kc & 1)]);      // releases `special`
+            }
+            __syncwarp();
+            ++kc;
+          } else if (lane == 0) {
+            mbar_arrive(&vempty[s]);
+          }
+          if (!refill(k)) {
+            ok = false;
+            break;
           }
         }
-        if (!ok || !walk.next(a)) break;
-      }
+        ++item;
+      } while (ok && walk.next(a));
     } else {
-      // ---------------------------------------------------------- Q, K, S = Q K^T
-      const uint32_t sQa = smem_u32(sQ);
-      TreeWalk qw = walk;                       // the tile whose Q is loaded next
+      // ---------------------------------------------------------- Q, S = Q K^T
+      const uint32_t sQa = smem_u32(sQ) + c * C::kQBufs * C::kQBytes;
+      TreeWalk qw = walk;                         // the piece whose Q is loaded next
       bool q_more = true;
-      int q_issued = 0;
+      int q_issued = 0, qi = 0;                   // Q tiles loaded, in use
       auto load_q = [&]() {
-        const int buf = q_issued % C::kQBufs;
+        while (q_more && qw.tile * a.TT + c * a.TC >= qw.q.T) q_more = qw.next(a);
+        if (!q_more) return;
+        const int buf = c * C::kQBufs + q_issued % C::kQBufs;
         if (lane == 0) {
-          const int tok = a.starts[qw.r] + qw.tile * a.TT;
-          mbar_expect_tx(&q_full[buf], C::kChunks * a.TT * a.G * 128);
+          const int tok = a.starts[qw.r] + qw.tile * a.TT + c * a.TC;
+          mbar_expect_tx(&q_full[buf], C::kChunks * a.TC * a.G * 128);
 #pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(sQ + buf * C::kQBytes + c * C::kQChunkBytes, &tmQ, 0, qw.head * a.G, tok, c, &q_full[buf]);
+          for (int x = 0; x < C::kChunks; ++x)
+            tma_load_4d(sQ + buf * C::kQBytes + x * C::kQChunkBytes, &tmQ, 0, qw.head * a.G, tok, x, &q_full[buf]);
         }
         __syncwarp();
         ++q_issued;
         q_more = qw.next(a);
       };
       for (int b = 0; b < C::kQBufs && q_more; ++b) load_q();
-      for (int item = 0; ok; ++item) {
-        const int buf = item % C::kQBufs;
-        if (!warp_wait(&q_full[buf], static_cast<uint32_t>(item / C::kQBufs) & 1u, abort_flag)) break;
+      do {
+        const bool act = walk.tile * a.TT + c * a.TC < walk.q.T;
+        const int buf = qi % C::kQBufs;
+        if (act && !warp_wait(&q_full[c * C::kQBufs + buf], static_cast<uint32_t>(qi / C::kQBufs) & 1u, abort_flag))
+          break;
         for (int i = 0; i < walk.n; ++i, ++k) {
           const int s = k % C::ST;
-          if ((k > 1 && !warp_wait(&pv_done[k & 1], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag)) ||
-              !warp_wait(&full[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+          if ((act && kc > 1 &&
+               !warp_wait(&pv_done[2 * c + (kc & 1)], static_cast<uint32_t>((kc - 2) >> 1) & 1u, abort_flag)) ||
+              !warp_wait(&kfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (lane == 0) {
+          if (act) {
+            tc_fence_after();
+            if (lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk & 3) * 32;
-              const uint64_t ad =
-                  sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
-              const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
-              tc_mma_ss(tmem_base + C::kColS + (k & 1) * 64, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk & 3) * 32;
+                const uint64_t ad = sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
+                const uint64_t bd =
+                    sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
+                tc_mma_ss(tS + (kc & 1) * 64, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&s_full[2 * c + (kc & 1)]);
+              tc_commit(&kempty[s]);
             }
-            tc_commit(&s_full[k & 1]);
-            tc_commit(&empty[s]);
+            __syncwarp();
+            ++kc;
+          } else if (lane == 0) {
+            mbar_arrive(&kempty[s]);
           }
-          __syncwarp();
-          // the stage, and after a tile's last block its Q, may be overwritten
-          if (!warp_wait(&empty[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+          if (!refill(k)) {
             ok = false;
             break;
           }
-          if (ld.more) load_next();
         }
         if (!ok) break;
-        if (q_more) load_q();
-        if (!walk.next(a)) break;
-      }
+        if (act) {
+          ++qi;
+          if (q_more) {                           // the tile's last S done: its Q may be overwritten
+            if (!warp_wait(&s_full[2 * c + ((kc - 1) & 1)], static_cast<uint32_t>((kc - 1) >> 1) & 1u, abort_flag))
+              break;
+            load_q();
+          }
+        }
+      } while (walk.next(a));
       for (int b = max(0, q_issued - C::kQBufs); b < q_issued; ++b)   // (bounded; complete unless aborted)
-        if (lane == 0) mbar_wait_drain(&q_full[b % C::kQBufs], static_cast<uint32_t>(b / C::kQBufs) & 1u);
+        if (lane == 0)
+          mbar_wait_drain(&q_full[c * C::kQBufs + b % C::kQBufs], static_cast<uint32_t>(b / C::kQBufs) & 1u);
     }
     if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
     // every load and product that was issued has finished before the CTA leaves (bounded)
@@ -679,19 +721,23 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
   } else {
     // ------------------------------------------------------------ softmax warps
+    const int c = (warp - 2 * NC) >> 2;            // the chain
     const int wq = warp & 3;                       // TMEM lane quadrant: rows 32*wq ..
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_addr = tmem_base + lane_bits + C::kColS;
-    const uint32_t o_addr = tmem_base + lane_bits + C::kColO;
+    const uint32_t s_addr = tmem_base + lane_bits + c * C::kChainCols + C::kColS;
+    const uint32_t o_addr = tmem_base + lane_bits + c * C::kChainCols + C::kColO;
+    s_full += 2 * c;
+    p_full += 2 * c;
+    pv_done += 2 * c;
     const int row = wq * 32 + lane;
-    const int row_t = row / a.G, row_g = row - row_t * a.G;   // token of the tile, head of the group
+    const int row_t = row / a.G, row_g = row - row_t * a.G;   // token of the chain's part, head of the group
     bool alive = true;
-    int k = 0;                                     // blocks of the share
+    int k = 0;                                     // blocks of the chain
     for (int item = 0; alive; ++item) {
-      const int t0 = walk.tile * a.TT;
-      const int rows = min(a.TT, walk.q.T - t0) * a.G;        // rows of the tile that exist
+      const int t0 = walk.tile * a.TT + c * a.TC;
+      const int rows = min(a.TC, walk.q.T - t0) * a.G;        // rows of the chain that exist
       if (wq * 32 >= rows) {
-        for (int i = 0; i < walk.n; ++i, ++k) {
+        for (int i = 0; rows > 0 && i < walk.n; ++i, ++k) {
           if (!warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
             alive = false;
             break;
@@ -704,7 +750,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const bool valid = row < rows;
       const int t = t0 + row_t;
       const long long token = static_cast<long long>(a.starts[walk.r]) + t;
-      const int open = masked ? walk.q.L : walk.q.L + t0 + 1;
+      const int open = masked ? walk.q.L : walk.q.L + t0 + 1;   // every row of the chain sees the keys before it
       float m_ref = -INFINITY, l = 0.f;
       float s0[32], s1[32];                        // S(k) of the row: columns 0..31 and 32..63
       if (warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
@@ -798,9 +844,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       tc_fence_after();
       const bool whole_row = walk.b0 == 0 && walk.n == walk.nbt;
       const float mul = whole_row ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // a NaN sum stays one
-      const bool fix = special[item & 1] == item + 1;
+      const bool fix = special[item & 15] == item + 1;
       const int hq = walk.head * a.G + row_g;
-      const long long prow = (2LL * cta + (walk.b0 == 0 ? 1 : 0)) * (a.TT * a.G) + row;
+      const long long prow = (2LL * cta + (walk.b0 == 0 ? 1 : 0)) * (a.TT * a.G) + c * a.TC * a.G + row;
       uint16_t* orow = static_cast<uint16_t*>(a.O) + token * a.o_token + hq * a.o_head;
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
@@ -814,12 +860,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             for (int x = 0; x < 32; ++x) o[x] = 0.f;
           }
           if (fix) {
-            // the elements taken out of V, for the rows that see their token
+            // the elements taken out of V (from the tile's `open` on), for the rows that see their token
+            const int out0 = masked ? walk.q.L : walk.q.L + walk.tile * a.TT + 1;
             const int* trow = a.table + static_cast<long long>(walk.r) * a.width;
             for (int kb = walk.b0 * kBlock; kb < (walk.b0 + walk.n) * kBlock; kb += kBlock) {
-              if (kb + kBlock <= open) continue;
+              if (kb + kBlock <= out0) continue;
               unsigned long long vis = tree_visible(a, walk.q.L, walk.q.T, t, token, kb);
-              if (open > kb) vis &= ~low_bits64(open - kb);
+              if (out0 > kb) vis &= ~low_bits64(out0 - kb);
               for (; vis; vis &= vis - 1) {
                 const int at = kb + __ffsll(static_cast<long long>(vis)) - 1;
                 const int id = trow[at >> a.page_shift];
@@ -862,9 +909,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::kTmemCols);
+    tmem_dealloc(tmem_base, NC * C::kChainCols);
   }
 }
 
