@@ -81,7 +81,7 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
 template <int D, int NC, bool kSmallQ>
 struct TreeCfg {
   static_assert(!(kSmallQ && NC > 1), "a small tile is one chain");
-  static constexpr int kThreads = 192 * NC;         // 2 issue and 4 softmax warps for each chain
+  static constexpr int kThreads = 256 * NC;                // 4 NC warps that issue, 4 NC softmax warps
   static constexpr int kCtas = NC == 1 ? 2 : 1;            // on an SM
   static constexpr int kChunks = D / 64;
   static constexpr int kQRows = kSmallQ ? 32 : 128;
@@ -92,18 +92,16 @@ struct TreeCfg {
   static constexpr int kKVBytes = kChunks * kKVChunkBytes;
   static constexpr int ST =                                // stages of K and of V
       NC == 2 ? (D == 64 ? 10 : 5) : (D == 64 ? (kSmallQ ? 6 : 5) : (kSmallQ ? 3 : 2));
-  // a stage is refilled this many blocks after its product was issued: with two chains
-  // the other one's product of the block has to be done too
-  static constexpr int kLag = NC == 2 ? 2 : 0;
+  static constexpr int kPieces = 8;                        // ring of piece descriptors, see TreePiece
   static constexpr int oQ = 0;
   static constexpr int oK = oQ + NC * kQBufs * kQBytes;
   static constexpr int oV = oK + ST * kKVBytes;
   static constexpr int oBar = oV + ST * kKVBytes;
-  static constexpr int kNumBars = 5 * ST + NC * (kQBufs + 6) + 1;
+  static constexpr int kNumBars = 5 * ST + 2 * kPieces + NC * (2 * kQBufs + 6) + 1;
   static constexpr int oMisc = oBar + kNumBars * 8;
-  static constexpr int kSmemBytes = oMisc + 512;
+  static constexpr int oPieces = oMisc + 16 * 4 + kThreads / 32 * 8;
+  static constexpr int kSmemBytes = oPieces + kPieces * 48;
   static constexpr uint32_t kColS = 0, kColO = 128, kChainCols = 256;   // S(k), then P(k): kColS + 64 (k & 1)
-  static_assert(ST < 16, "the ring of `special`");
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -194,6 +192,16 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// tcgen05.st of 16 packed 32-bit values to this warp's lanes.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
@@ -320,6 +328,15 @@ struct TreeWalk {
   }
 };
 
+// What the other warps need to know of a piece, from the load warp in a ring of kPieces.
+struct TreePiece {
+  int r, tok0, L, T;              // request, its first row of the step, cached and new tokens
+  int head, tile, b0, n, nbt;     // key head, tile, first block, blocks of the piece and of the whole tile
+  int last;                       // 1: the share's last piece
+  int special;                    // 1: an element of V was taken out
+  int pad;
+};
+
 // A walk block by block, for the loads. The lanes hold the ids of the 32 pages from `base`
 // on, and of the 32 behind them, read a window ahead of their use: a read of one id a
 // block cost its warp 700 cycles a block. (A block's pages never lie in two windows.)
@@ -373,9 +390,12 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   uint64_t* kempty = kfull + C::ST;        // [ST] K stage consumed by every chain's S MMA
   uint64_t* vfull = kempty + C::ST;        // [ST] V stage loaded
   uint64_t* vempty = vfull + C::ST;        // [ST] V stage consumed by every chain's P.V MMA
-  uint64_t* vready = vempty + C::ST;       // [ST] V stage loaded and its unseen rows dealt with (two chains)
-  uint64_t* q_full = vready + C::ST;       // [NC][kQBufs] Q of a tile loaded
-  uint64_t* s_full = q_full + NC * C::kQBufs;   // [NC][2] by block parity: S(k) written by the MMA
+  uint64_t* vready = vempty + C::ST;       // [ST] V stage loaded and its unseen rows dealt with
+  uint64_t* piece_full = vready + C::ST;   // [kPieces] piece written
+  uint64_t* piece_empty = piece_full + C::kPieces;  // [kPieces] piece read by every other warp with a part in it
+  uint64_t* q_full = piece_empty + C::kPieces;   // [NC][kQBufs] Q of a tile loaded
+  uint64_t* q_empty = q_full + NC * C::kQBufs;  // [NC][kQBufs] the S MMAs of the Q's piece finished
+  uint64_t* s_full = q_empty + NC * C::kQBufs;  // [NC][2] by block parity: S(k) written by the MMA
   uint64_t* p_full = s_full + 2 * NC;      // [NC][2] by block parity: P(k) in TMEM and O corrected
   uint64_t* pv_done = p_full + 2 * NC;     // [NC][2] by block parity: P(k).V finished (the MMA and `special`)
   uint64_t* drain = pv_done + 2 * NC;      // every MMA of the CTA finished
@@ -383,9 +403,9 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   volatile int* abort_flag = misc + 0;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 1);
   int* found = misc + 2;                   // the share's first request, its T and L
-  volatile int* special = misc + 8;        // [16] by piece: 1 + a piece of which an element of V was taken out
-  long long* found_at = reinterpret_cast<long long*>(misc + 24);  // the request's first block on the line
-  long long* wsum = reinterpret_cast<long long*>(misc + 26);      // [kWarps]
+  long long* found_at = reinterpret_cast<long long*>(misc + 8);   // the request's first block on the line
+  long long* wsum = reinterpret_cast<long long*>(misc + 16);      // [kWarps]
+  TreePiece* pieces = reinterpret_cast<TreePiece*>(base + C::oPieces);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned FULL = 0xffffffffu;
@@ -399,7 +419,14 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       mbar_init(&vempty[s], NC);
       mbar_init(&vready[s], 1);
     }
-    for (int b = 0; b < NC * C::kQBufs; ++b) mbar_init(&q_full[b], 1);
+    for (int b = 0; b < C::kPieces; ++b) {
+      mbar_init(&piece_full[b], 1);
+      mbar_init(&piece_empty[b], 1 + 6 * NC);
+    }
+    for (int b = 0; b < NC * C::kQBufs; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_empty[b], 1);
+    }
     for (int b = 0; b < 2 * NC; ++b) {
       mbar_init(&s_full[b], 1);
       mbar_init(&p_full[b], 4);
@@ -408,7 +435,6 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     mbar_init(drain, 2 * NC);
     fence_mbar_init();
     *abort_flag = 0;
-    for (int b = 0; b < 16; ++b) special[b] = 0;
     found[0] = -1;
   }
   bool bad = false;
@@ -505,223 +531,270 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   const bool loads = subs == 1 ? lane == 0 : my_chunk < C::kChunks;
   const int sub_off = my_sub * sub, dst_off = my_chunk * C::kKVChunkBytes + sub_off * 128;
 
-  if (warp == 0) tmem_alloc(tmem_holder, NC * C::kChainCols);
+  if (warp == 1) tmem_alloc(tmem_holder, NC * C::kChainCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  // piece `item` of the share, once the load warp has written it; null if a wait was given up
+  auto piece = [&](int item) -> TreePiece* {
+    if (!warp_wait(&piece_full[item % C::kPieces], static_cast<uint32_t>(item / C::kPieces) & 1u, abort_flag))
+      return nullptr;
+    return &pieces[item % C::kPieces];
+  };
+  auto release = [&](int item) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[item % C::kPieces]);
+  };
+  // the chain has rows in the piece
+  auto active = [&](const TreePiece* p, int c) { return p->tile * a.TT + c * a.TC < p->T; };
 
-  if (warp < 2 * NC) {
-    // Issue warps: 0 .. NC-1 the P V products, NC .. 2NC-1 the S products of a chain. Warp
-    // 0 loads V, warp NC loads K: stage k % ST holds block k of the share, refilled when the
-    // products that read block k - ST have completed.
-    const bool is_v = warp < NC;
-    const int c = is_v ? warp : warp - NC;
-    const bool loader = c == 0;
-    uint8_t* ring = is_v ? sV : sK;
-    uint64_t* full = is_v ? vfull : kfull;
-    uint64_t* empty = is_v ? vempty : kempty;
-    const CUtensorMap* map = is_v ? &tmV : &tmK;
+  if (warp == 0) {
+    // ------------------------------------------------------------ pieces, K and V loads
+    // stage k % ST holds block k of the share, loaded when the products that read block
+    // k - ST have completed
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
     bool bad_page = false;
     TreeLoad ld;
     ld.w = walk;
-    ld.more = loader;
-    int issued = 0;
-    auto load_next = [&]() {
-      const int s = issued % C::ST;
+    ld.more = true;
+    ld.open(a, lane);
+    int nk = 0, nv = 0, item = 0;                 // loads issued, pieces written
+    while (ld.more) {
+      const int s = nk % C::ST;
+      const uint32_t before = static_cast<uint32_t>(nk / C::ST - 1) & 1u;
       const int at = (ld.w.b0 + ld.k) * kBlock + sub_off, keys = ld.w.q.L + ld.w.q.T;   // the lane's box
       const int boxes = (min(keys - at + sub_off, kBlock) + sub - 1) >> sub_shift;
+      const uint32_t bytes = static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks;
       int id = __shfl_sync(FULL, ld.ids, (at >> a.page_shift) - ld.base);
-      if (lane == 0) mbar_expect_tx(&full[s], static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks);
-      __syncwarp();
-      if (loads && at < keys) {
-        if (id < 0 || id >= a.pages) {
-          bad_page = true;
-          id = 0;                                 // flagged; any page of the pool keeps the load in bounds
-        }
-        tma_load_5d(ring + s * C::kKVBytes + dst_off, map, 0, at & (page - 1), my_chunk, ld.w.head, id, &full[s]);
+      const bool mine_loads = loads && at < keys;
+      if (mine_loads && (id < 0 || id >= a.pages)) {
+        bad_page = true;
+        id = 0;                                   // flagged; any page of the pool keeps the load in bounds
       }
-      ++issued;
-      ld.step(a, lane);
-    };
-    if (loader) {
-      if (lane == 0) tma_prefetch_desc(map);
-      ld.open(a, lane);
-      for (int s = 0; s < C::ST && ld.more; ++s) load_next();
-    }
-    // after block k's product was issued: the stage of block k - kLag gets block k - kLag + ST
-    auto refill = [&](int k) {
-      if (!ld.more || k < C::kLag) return true;
-      const int b = k - C::kLag;
-      if (!warp_wait(&empty[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u, abort_flag)) return false;
-      load_next();
-      return true;
-    };
-    const uint32_t ring_a = smem_u32(ring);
-    const uint32_t tS = tmem_base + c * C::kChainCols + C::kColS, tO = tmem_base + c * C::kChainCols + C::kColO;
-    int k = 0, kc = 0;                            // blocks of the share, of the chain
-    bool ok = true;
-    if (is_v) {
-      // ---------------------------------------------------------- O += P V
-      int item = 0;
-      do {
-        const bool act = walk.tile * a.TT + c * a.TC < walk.q.T;
-        const int keys = walk.q.L + walk.q.T;
-        // every row of the tile sees the keys before `open`; from there on rows differ
-        const int open = masked ? walk.q.L : walk.q.L + walk.tile * a.TT + 1;
-        bool taken_out = false;
-        for (int i = 0; i < walk.n; ++i, ++k) {
-          const int s = k % C::ST;
-          if (!warp_wait(c == 0 ? &vfull[s] : &vready[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int kb = (walk.b0 + i) * kBlock;
-          if (c == 0 && kb + kBlock > open) {
-            // rows behind the last token to zero; elements that are not finite out of
-            // the rows that not every query sees
-            const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
-            uint8_t* v = ring + s * C::kKVBytes;
-            for (int h = 0; h < C::kChunks; ++h) {
-              for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
-                uint4* at = reinterpret_cast<uint4*>(v + h * C::kKVChunkBytes + x * 16);
-                if (x >= live * 8) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  uint4 w = *at;
-                  uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-                  bool any = false;
-#pragma unroll
-                  for (int u = 0; u < 4; ++u) {
-                    const bool lo = not_finite16<kElem>(e[u]), hi = not_finite16<kElem>(e[u] >> 16);
-                    if (lo) e[u] &= 0xffff0000u;
-                    if (hi) e[u] &= 0x0000ffffu;
-                    any |= lo | hi;
-                  }
-                  if (any) {
-                    *at = w;
-                    taken_out = true;
-                  }
-                }
-              }
-            }
-            fence_proxy_async_smem();
-            if (__any_sync(FULL, taken_out) && lane == 0) special[item & 15] = item + 1;
-            __syncwarp();
-          }
-          if (NC > 1 && c == 0 && lane == 0) mbar_arrive(&vready[s]);
-          if (act) {
-            if (!warp_wait(&p_full[2 * c + (kc & 1)], static_cast<uint32_t>(kc >> 1) & 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-              for (int kk = 0; kk < kBlock / 16; ++kk) {
-                const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
-                tc_mma_ts(tO, tS + (kc & 1) * 64 + kk * 8, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
-              }
-              tc_commit(&pv_done[2 * c + (kc & 1)]);
-              tc_commit(&vempty[s]);
-              mbar_arrive(&pv_done[2 * c + (kc & 1)]);      // releases `special`
-            }
-            __syncwarp();
-            ++kc;
-          } else if (lane == 0) {
-            mbar_arrive(&vempty[s]);
-          }
-          if (!refill(k)) {
-            ok = false;
-            break;
-          }
+      if (nk >= C::ST && !warp_wait(&kempty[s], before, abort_flag)) break;
+      if (ld.k == 0 && item >= C::kPieces &&
+          !warp_wait(&piece_empty[item % C::kPieces], static_cast<uint32_t>(item / C::kPieces - 1) & 1u, abort_flag))
+        break;
+      if (lane == 0) {
+        mbar_expect_tx(&kfull[s], bytes);
+        if (ld.k == 0) {
+          TreePiece* p = &pieces[item % C::kPieces];
+          p->r = ld.w.r;
+          p->tok0 = a.starts[ld.w.r];
+          p->L = ld.w.q.L;
+          p->T = ld.w.q.T;
+          p->head = ld.w.head;
+          p->tile = ld.w.tile;
+          p->b0 = ld.w.b0;
+          p->n = ld.w.n;
+          p->nbt = ld.w.nbt;
+          p->last = ld.w.left == ld.w.n && ld.w.kr < 0;
+          p->special = 0;
+          mbar_arrive(&piece_full[item % C::kPieces]);
         }
-        ++item;
-      } while (ok && walk.next(a));
-    } else {
-      // ---------------------------------------------------------- Q, S = Q K^T
-      const uint32_t sQa = smem_u32(sQ) + c * C::kQBufs * C::kQBytes;
-      TreeWalk qw = walk;                         // the piece whose Q is loaded next
-      bool q_more = true;
-      int q_issued = 0, qi = 0;                   // Q tiles loaded, in use
-      auto load_q = [&]() {
-        while (q_more && qw.tile * a.TT + c * a.TC >= qw.q.T) q_more = qw.next(a);
-        if (!q_more) return;
-        const int buf = c * C::kQBufs + q_issued % C::kQBufs;
+      }
+      __syncwarp();
+      if (mine_loads)
+        tma_load_5d(sK + s * C::kKVBytes + dst_off, &tmK, 0, at & (page - 1), my_chunk, ld.w.head, id, &kfull[s]);
+      ++nk;
+      if (ld.k == 0) ++item;
+      if (nk > C::ST && !warp_wait(&vempty[s], before, abort_flag)) break;
+      if (lane == 0) mbar_expect_tx(&vfull[s], bytes);
+      __syncwarp();
+      if (mine_loads)
+        tma_load_5d(sV + s * C::kKVBytes + dst_off, &tmV, 0, at & (page - 1), my_chunk, ld.w.head, id, &vfull[s]);
+      ++nv;
+      ld.step(a, lane);
+    }
+    if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
+    // every load that was issued has landed before the CTA leaves (bounded)
+    if (lane == 0) {
+      for (int b = max(0, nk - C::ST); b < nk; ++b)
+        mbar_wait_drain(&kfull[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
+      for (int b = max(0, nv - C::ST); b < nv; ++b)
+        mbar_wait_drain(&vfull[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ Q loads, what a V block holds unseen
+    if (lane == 0) tma_prefetch_desc(&tmQ);
+    int k = 0, nq[NC] = {};                       // blocks of the share, Q tiles loaded of each chain
+    bool ok = true;
+    for (int item = 0; ok; ++item) {
+      TreePiece* p = piece(item);
+      if (!p) break;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (!ok || !active(p, c)) continue;
+        const int buf = c * C::kQBufs + nq[c] % C::kQBufs;
+        if (nq[c] >= C::kQBufs &&
+            !warp_wait(&q_empty[buf], static_cast<uint32_t>(nq[c] / C::kQBufs - 1) & 1u, abort_flag)) {
+          ok = false;
+          continue;
+        }
         if (lane == 0) {
-          const int tok = a.starts[qw.r] + qw.tile * a.TT + c * a.TC;
           mbar_expect_tx(&q_full[buf], C::kChunks * a.TC * a.G * 128);
 #pragma unroll
           for (int x = 0; x < C::kChunks; ++x)
-            tma_load_4d(sQ + buf * C::kQBytes + x * C::kQChunkBytes, &tmQ, 0, qw.head * a.G, tok, x, &q_full[buf]);
+            tma_load_4d(sQ + buf * C::kQBytes + x * C::kQChunkBytes, &tmQ, 0, p->head * a.G,
+                        p->tok0 + p->tile * a.TT + c * a.TC, x, &q_full[buf]);
         }
         __syncwarp();
-        ++q_issued;
-        q_more = qw.next(a);
-      };
-      for (int b = 0; b < C::kQBufs && q_more; ++b) load_q();
-      do {
-        const bool act = walk.tile * a.TT + c * a.TC < walk.q.T;
-        const int buf = qi % C::kQBufs;
-        if (act && !warp_wait(&q_full[c * C::kQBufs + buf], static_cast<uint32_t>(qi / C::kQBufs) & 1u, abort_flag))
+        ++nq[c];
+      }
+      const int keys = p->L + p->T, n = p->n, b0 = p->b0, last = p->last;
+      // every row of the tile sees the keys before `open`; from there on rows differ
+      const int open = masked ? p->L : p->L + p->tile * a.TT + 1;
+      for (int i = 0; ok && i < n; ++i, ++k) {
+        const int s = k % C::ST;
+        if (!warp_wait(&vfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+          ok = false;
           break;
-        for (int i = 0; i < walk.n; ++i, ++k) {
-          const int s = k % C::ST;
-          if ((act && kc > 1 &&
-               !warp_wait(&pv_done[2 * c + (kc & 1)], static_cast<uint32_t>((kc - 2) >> 1) & 1u, abort_flag)) ||
-              !warp_wait(&kfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (act) {
-            tc_fence_after();
-            if (lane == 0) {
+        }
+        const int kb = (b0 + i) * kBlock;
+        if (kb + kBlock > open) {
+          // rows behind the last token to zero; elements that are not finite out of
+          // the rows that not every query sees
+          const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
+          bool taken_out = false;
+          uint8_t* v = sV + s * C::kKVBytes;
+          for (int h = 0; h < C::kChunks; ++h) {
+            for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
+              uint4* at = reinterpret_cast<uint4*>(v + h * C::kKVChunkBytes + x * 16);
+              if (x >= live * 8) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                uint4 w = *at;
+                uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+                bool any = false;
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk & 3) * 32;
-                const uint64_t ad = sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
-                const uint64_t bd =
-                    sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
-                tc_mma_ss(tS + (kc & 1) * 64, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+                for (int u = 0; u < 4; ++u) {
+                  const bool lo = not_finite16<kElem>(e[u]), hi = not_finite16<kElem>(e[u] >> 16);
+                  if (lo) e[u] &= 0xffff0000u;
+                  if (hi) e[u] &= 0x0000ffffu;
+                  any |= lo | hi;
+                }
+                if (any) {
+                  *at = w;
+                  taken_out = true;
+                }
               }
-              tc_commit(&s_full[2 * c + (kc & 1)]);
-              tc_commit(&kempty[s]);
             }
-            __syncwarp();
-            ++kc;
-          } else if (lane == 0) {
-            mbar_arrive(&kempty[s]);
           }
-          if (!refill(k)) {
-            ok = false;
-            break;
-          }
+          fence_proxy_async_smem();
+          if (__any_sync(FULL, taken_out) && lane == 0) p->special = 1;
+          __syncwarp();
         }
-        if (!ok) break;
-        if (act) {
-          ++qi;
-          if (q_more) {                           // the tile's last S done: its Q may be overwritten
-            if (!warp_wait(&s_full[2 * c + ((kc - 1) & 1)], static_cast<uint32_t>((kc - 1) >> 1) & 1u, abort_flag))
-              break;
-            load_q();
-          }
-        }
-      } while (walk.next(a));
-      for (int b = max(0, q_issued - C::kQBufs); b < q_issued; ++b)   // (bounded; complete unless aborted)
-        if (lane == 0)
+        if (lane == 0) mbar_arrive(&vready[s]);
+      }
+      release(item);
+      if (last) break;
+    }
+    if (lane == 0) {                              // (bounded; complete unless aborted)
+      for (int c = 0; c < NC; ++c)
+        for (int b = max(0, nq[c] - C::kQBufs); b < nq[c]; ++b)
           mbar_wait_drain(&q_full[c * C::kQBufs + b % C::kQBufs], static_cast<uint32_t>(b / C::kQBufs) & 1u);
     }
-    if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
-    // every load and product that was issued has finished before the CTA leaves (bounded)
-    if (lane == 0) {
+  } else if (warp < 2 + NC) {
+    // ------------------------------------------------------------ S = Q K^T of chain c
+    const int c = warp - 2;
+    const uint32_t tS = tmem_base + c * C::kChainCols + C::kColS;
+    const uint32_t ring_a = smem_u32(sK), sQa = smem_u32(sQ) + c * C::kQBufs * C::kQBytes;
+    int k = 0, kc = 0, nq = 0;                    // blocks of the share, of the chain, tiles of the chain
+    bool ok = true;
+    for (int item = 0; ok; ++item) {
+      const TreePiece* p = piece(item);
+      if (!p) break;
+      const bool act = active(p, c);
+      const int n = p->n, last = p->last, buf = nq % C::kQBufs;
+      release(item);
+      if (act && !warp_wait(&q_full[c * C::kQBufs + buf], static_cast<uint32_t>(nq / C::kQBufs) & 1u, abort_flag))
+        break;
+      for (int i = 0; i < n; ++i, ++k) {
+        const int s = k % C::ST;
+        if ((act && kc > 1 &&
+             !warp_wait(&pv_done[2 * c + (kc & 1)], static_cast<uint32_t>((kc - 2) >> 1) & 1u, abort_flag)) ||
+            !warp_wait(&kfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (!act) {
+          if (lane == 0) mbar_arrive(&kempty[s]);
+          continue;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk & 3) * 32;
+            const uint64_t ad = sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
+            const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
+            tc_mma_ss(tS + (kc & 1) * 64, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[2 * c + (kc & 1)]);
+          tc_commit(&kempty[s]);
+          if (i + 1 == n) tc_commit(&q_empty[c * C::kQBufs + buf]);
+        }
+        __syncwarp();
+        ++kc;
+      }
+      if (act) ++nq;
+      if (last) break;
+    }
+    if (lane == 0) {                              // (bounded)
       tc_commit(drain);
       mbar_wait_drain(drain, 0u);
-      for (int b = max(0, issued - C::ST); b < issued; ++b)
-        mbar_wait_drain(&full[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
     }
-  } else {
+  } else if (warp < 2 + 2 * NC) {
+    // ------------------------------------------------------------ O += P V of chain c
+    const int c = warp - 2 - NC;
+    const uint32_t tP = tmem_base + c * C::kChainCols + C::kColS, tO = tmem_base + c * C::kChainCols + C::kColO;
+    const uint32_t ring_a = smem_u32(sV);
+    int k = 0, kc = 0;                            // blocks of the share, of the chain
+    bool ok = true;
+    for (int item = 0; ok; ++item) {
+      const TreePiece* p = piece(item);
+      if (!p) break;
+      const bool act = active(p, c);
+      const int n = p->n, last = p->last;
+      release(item);
+      for (int i = 0; i < n; ++i, ++k) {
+        const int s = k % C::ST;
+        if (!warp_wait(&vready[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag) ||
+            (act && !warp_wait(&p_full[2 * c + (kc & 1)], static_cast<uint32_t>(kc >> 1) & 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (!act) {
+          if (lane == 0) mbar_arrive(&vempty[s]);
+          continue;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < kBlock / 16; ++kk) {
+            const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
+            tc_mma_ts(tO, tP + (kc & 1) * 64 + kk * 8, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit(&pv_done[2 * c + (kc & 1)]);
+          tc_commit(&vempty[s]);
+          mbar_arrive(&pv_done[2 * c + (kc & 1)]);      // passes on the piece's `special`, seen through vready
+        }
+        __syncwarp();
+        ++kc;
+      }
+      if (last) break;
+    }
+    if (lane == 0) {                              // (bounded)
+      tc_commit(drain);
+      mbar_wait_drain(drain, 0u);
+    }
+  } else if (warp >= 4 * NC) {
     // ------------------------------------------------------------ softmax warps
-    const int c = (warp - 2 * NC) >> 2;            // the chain
+    const int c = (warp - 4 * NC) >> 2;            // the chain
     const int wq = warp & 3;                       // TMEM lane quadrant: rows 32*wq ..
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t s_addr = tmem_base + lane_bits + c * C::kChainCols + C::kColS;
@@ -730,27 +803,29 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     p_full += 2 * c;
     pv_done += 2 * c;
     const int row = wq * 32 + lane;
-    const int row_t = row / a.G, row_g = row - row_t * a.G;   // token of the chain's part, head of the group
     bool alive = true;
     int k = 0;                                     // blocks of the chain
     for (int item = 0; alive; ++item) {
-      const int t0 = walk.tile * a.TT + c * a.TC;
-      const int rows = min(a.TC, walk.q.T - t0) * a.G;        // rows of the chain that exist
+      const TreePiece* p = piece(item);
+      if (!p) break;
+      const int n = p->n, last = p->last;
+      const int t0 = p->tile * a.TT + c * a.TC;
+      const int rows = min(a.TC, p->T - t0) * a.G;            // rows of the chain that exist
       if (wq * 32 >= rows) {
-        for (int i = 0; rows > 0 && i < walk.n; ++i, ++k) {
+        for (int i = 0; rows > 0 && i < n; ++i, ++k) {
           if (!warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
             alive = false;
             break;
           }
           if (lane == 0) mbar_arrive(&p_full[k & 1]);
         }
-        if (!alive || !walk.next(a)) break;
+        release(item);
+        if (last) break;
         continue;
       }
       const bool valid = row < rows;
-      const int t = t0 + row_t;
-      const long long token = static_cast<long long>(a.starts[walk.r]) + t;
-      const int open = masked ? walk.q.L : walk.q.L + t0 + 1;   // every row of the chain sees the keys before it
+      const int b0 = p->b0;
+      const int open = masked ? p->L : p->L + t0 + 1;         // every row of the chain sees the keys before it
       float m_ref = -INFINITY, l = 0.f;
       float s0[32], s1[32];                        // S(k) of the row: columns 0..31 and 32..63
       if (warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
@@ -760,20 +835,23 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       } else {
         alive = false;
       }
-      for (int i = 0; alive && i < walk.n; ++i, ++k) {
-        const int kb = (walk.b0 + i) * kBlock;
+      for (int i = 0; alive && i < n; ++i, ++k) {
+        const int kb = (b0 + i) * kBlock;
         unsigned long long vis = ~0ull;
         const bool part = kb + kBlock > open;       // some row does not see the whole block
-        if (part) vis = valid ? tree_visible(a, walk.q.L, walk.q.T, t, token, kb) : 0ull;
+        if (part) {
+          const int t = t0 + row / a.G;
+          vis = valid ? tree_visible(a, p->L, p->T, t, static_cast<long long>(p->tok0) + t, kb) : 0ull;
+        }
         tmem_wait_ld();
         pin32(s0);
         pin32(s1);
         if (part) {
           const uint32_t vlo = static_cast<uint32_t>(vis), vhi = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            s0[c] = (vlo >> c) & 1u ? s0[c] : -INFINITY;
-            s1[c] = (vhi >> c) & 1u ? s1[c] : -INFINITY;
+          for (int x = 0; x < 32; ++x) {
+            s0[x] = (vlo >> x) & 1u ? s0[x] : -INFINITY;
+            s1[x] = (vhi >> x) & 1u ? s1[x] : -INFINITY;
           }
         }
         float mx[8];
@@ -797,12 +875,13 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         }
         const bool any_raise = __any_sync(FULL, raise);
         const float mref = (m_ref == -INFINITY) ? 0.f : m_ref;
-        uint32_t pk[32];
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
         const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2), nm2 = f2pack(-mref, -mref);
+        uint32_t pk[16];
         tree_exp32<kElem>(s0, sc2, nm2, acc0, acc1, pk);
-        tree_exp32<kElem>(s1, sc2, nm2, acc0, acc1, pk + 16);
-        tmem_st32u(s_addr + (k & 1) * 64, pk);
+        tmem_st16u(s_addr + (k & 1) * 64, pk);
+        tree_exp32<kElem>(s1, sc2, nm2, acc0, acc1, pk);
+        tmem_st16u(s_addr + (k & 1) * 64 + 16, pk);
         float r0, r1, r2, r3;
         f2unpack(acc0, r0, r1);
         f2unpack(acc1, r2, r3);
@@ -828,7 +907,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[k & 1]);
-        if (i + 1 < walk.n) {
+        if (i + 1 < n) {
           if (!warp_wait(&s_full[(k + 1) & 1], static_cast<uint32_t>((k + 1) >> 1) & 1u, abort_flag)) {
             alive = false;
             break;
@@ -839,14 +918,16 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         }
       }
       tmem_wait_ld();
-      // ------------------------------------------------------------ epilogue of the tile
+      // ------------------------------------------------------------ epilogue of the piece
       if (!alive || !warp_wait(&pv_done[(k - 1) & 1], static_cast<uint32_t>((k - 1) >> 1) & 1u, abort_flag)) break;
       tc_fence_after();
-      const bool whole_row = walk.b0 == 0 && walk.n == walk.nbt;
+      const bool whole_row = b0 == 0 && n == p->nbt;
       const float mul = whole_row ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;   // a NaN sum stays one
-      const bool fix = special[item & 15] == item + 1;
-      const int hq = walk.head * a.G + row_g;
-      const long long prow = (2LL * cta + (walk.b0 == 0 ? 1 : 0)) * (a.TT * a.G) + c * a.TC * a.G + row;
+      const bool fix = *reinterpret_cast<volatile const int*>(&p->special) != 0;
+      const int row_t = row / a.G, t = t0 + row_t;
+      const int hq = p->head * a.G + row - row_t * a.G;
+      const long long token = static_cast<long long>(p->tok0) + t;
+      const long long prow = (2LL * cta + (b0 == 0 ? 1 : 0)) * (a.TT * a.G) + c * a.TC * a.G + row;
       uint16_t* orow = static_cast<uint16_t*>(a.O) + token * a.o_token + hq * a.o_head;
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
@@ -861,17 +942,17 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
           }
           if (fix) {
             // the elements taken out of V (from the tile's `open` on), for the rows that see their token
-            const int out0 = masked ? walk.q.L : walk.q.L + walk.tile * a.TT + 1;
-            const int* trow = a.table + static_cast<long long>(walk.r) * a.width;
-            for (int kb = walk.b0 * kBlock; kb < (walk.b0 + walk.n) * kBlock; kb += kBlock) {
+            const int out0 = masked ? p->L : p->L + p->tile * a.TT + 1;
+            const int* trow = a.table + static_cast<long long>(p->r) * a.width;
+            for (int kb = b0 * kBlock; kb < (b0 + n) * kBlock; kb += kBlock) {
               if (kb + kBlock <= out0) continue;
-              unsigned long long vis = tree_visible(a, walk.q.L, walk.q.T, t, token, kb);
+              unsigned long long vis = tree_visible(a, p->L, p->T, t, token, kb);
               if (out0 > kb) vis &= ~low_bits64(out0 - kb);
               for (; vis; vis &= vis - 1) {
                 const int at = kb + __ffsll(static_cast<long long>(vis)) - 1;
                 const int id = trow[at >> a.page_shift];
                 if (id < 0 || id >= a.pages) continue;
-                const uint16_t* v = Vraw + id * v_page + (at & (page - 1)) * v_token + walk.head * v_head + cc;
+                const uint16_t* v = Vraw + id * v_page + (at & (page - 1)) * v_token + p->head * v_head + cc;
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
                   const uint32_t e = v[x];
@@ -903,13 +984,14 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         else if (a.lse)
           a.lse[token * (a.Hkv * a.G) + hq] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
       }
-      tc_fence_before();                            // O is read before the next tile's P is published
-      if (!walk.next(a)) break;
+      tc_fence_before();                            // O is read before the next piece's P is published
+      release(item);
+      if (last) break;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, NC * C::kChainCols);
   }
