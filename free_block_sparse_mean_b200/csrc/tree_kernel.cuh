@@ -249,16 +249,15 @@ __device__ __forceinline__ float to_float16(uint32_t bits) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
 }
 
-// p = 2^(s * sc - nm) for 32 columns of a row: P as 16-bit pairs, the sums of the p on
-// two pairs of accumulators.
+// p = 2^(s * sc + nm) for 32 columns of a row: P as 16-bit pairs, the sums of the p on
+// two pairs of accumulators. 334 cycles for a warp alone, 268 each for two on a scheduler
+// (the exponential unit's own bound is 256; with the multiply-add on pairs 388 and 280).
 template <int kElem>
-__device__ __forceinline__ void tree_exp32(const float (&s)[32], uint64_t sc2, uint64_t nm2, uint64_t& acc0,
-                                           uint64_t& acc1, uint32_t* pk) {
+__device__ __forceinline__ void tree_exp32(const float (&s)[32], float sc, float nm, uint64_t& acc0, uint64_t& acc1,
+                                           uint32_t* pk) {
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
-    float x0, x1;
-    f2unpack(ffma2(f2pack(s[c], s[c + 1]), sc2, nm2), x0, x1);
-    const float p0 = ex2(x0), p1 = ex2(x1);
+    const float p0 = ex2(fmaf(s[c], sc, nm)), p1 = ex2(fmaf(s[c + 1], sc, nm));
     if ((c >> 1) & 1)
       acc1 = fadd2(acc1, f2pack(p0, p1));
     else
@@ -876,11 +875,10 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         const bool any_raise = __any_sync(FULL, raise);
         const float mref = (m_ref == -INFINITY) ? 0.f : m_ref;
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-        const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2), nm2 = f2pack(-mref, -mref);
         uint32_t pk[16];
-        tree_exp32<kElem>(s0, sc2, nm2, acc0, acc1, pk);
+        tree_exp32<kElem>(s0, a.scale_log2, -mref, acc0, acc1, pk);
         tmem_st16u(s_addr + (k & 1) * 64, pk);
-        tree_exp32<kElem>(s1, sc2, nm2, acc0, acc1, pk);
+        tree_exp32<kElem>(s1, a.scale_log2, -mref, acc0, acc1, pk);
         tmem_st16u(s_addr + (k & 1) * 64 + 16, pk);
         float r0, r1, r2, r3;
         f2unpack(acc0, r0, r1);
