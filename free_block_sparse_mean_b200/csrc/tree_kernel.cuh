@@ -195,6 +195,14 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// True in one thread of the warp, the same one every time. The compiler keeps what is
+// uniform in such a branch in uniform registers, where an MMA takes its operands from.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // tcgen05.st of 16 packed 32-bit values to this warp's lanes.
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -406,8 +414,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   long long* wsum = reinterpret_cast<long long*>(misc + 16);      // [kWarps]
   TreePiece* pieces = reinterpret_cast<TreePiece*>(base + C::oPieces);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned FULL = 0xffffffffu;
+  const int warp = __shfl_sync(FULL, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   // ------------------------------------------------------------ set up, find this CTA's share
   if (threadIdx.x == 0) {
@@ -701,7 +709,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     // ------------------------------------------------------------ S = Q K^T of chain c
     const int c = warp - 2;
     const uint32_t tS = tmem_base + c * C::kChainCols + C::kColS;
-    const uint32_t ring_a = smem_u32(sK), sQa = smem_u32(sQ) + c * C::kQBufs * C::kQBytes;
+    const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ) + c * C::kQBufs * C::kQBytes, 16, 1024);
     int k = 0, kc = 0, nq = 0;                    // blocks of the share, of the chain, tiles of the chain
     bool ok = true;
     for (int item = 0; ok; ++item) {
@@ -709,6 +718,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       if (!p) break;
       const bool act = active(p, c);
       const int n = p->n, last = p->last, buf = nq % C::kQBufs;
+      const uint64_t dq = dQ + buf * (C::kQBytes >> 4);
       release(item);
       if (act && !warp_wait(&q_full[c * C::kQBufs + buf], static_cast<uint32_t>(nq / C::kQBufs) & 1u, abort_flag))
         break;
@@ -725,13 +735,14 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
           continue;
         }
         tc_fence_after();
-        if (lane == 0) {
+        const uint64_t dk = dK + s * (C::kKVBytes >> 4);
+        const uint32_t tD = tS + (kc & 1) * 64;
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk & 3) * 32;
-            const uint64_t ad = sdesc_sw128(sQa + buf * C::kQBytes + (kk >> 2) * C::kQChunkBytes + off, 16, 1024);
-            const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + (kk >> 2) * C::kKVChunkBytes + off, 16, 1024);
-            tc_mma_ss(tS + (kc & 1) * 64, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+            const uint32_t off = (kk & 3) * 2;            // 16 columns, in 16-byte steps
+            tc_mma_ss(tD, dq + (kk >> 2) * (C::kQChunkBytes >> 4) + off, dk + (kk >> 2) * (C::kKVChunkBytes >> 4) + off,
+                      kIdescS, kk > 0 ? 1u : 0u);
           }
           tc_commit(&s_full[2 * c + (kc & 1)]);
           tc_commit(&kempty[s]);
@@ -743,7 +754,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       if (act) ++nq;
       if (last) break;
     }
-    if (lane == 0) {                              // (bounded)
+    if (elect_one()) {                            // (bounded)
       tc_commit(drain);
       mbar_wait_drain(drain, 0u);
     }
@@ -751,7 +762,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     // ------------------------------------------------------------ O += P V of chain c
     const int c = warp - 2 - NC;
     const uint32_t tP = tmem_base + c * C::kChainCols + C::kColS, tO = tmem_base + c * C::kChainCols + C::kColO;
-    const uint32_t ring_a = smem_u32(sV);
+    const uint64_t dV = sdesc_sw128(smem_u32(sV), C::kKVChunkBytes, 1024);
     int k = 0, kc = 0;                            // blocks of the share, of the chain
     bool ok = true;
     for (int item = 0; ok; ++item) {
@@ -772,12 +783,12 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
           continue;
         }
         tc_fence_after();
-        if (lane == 0) {
+        const uint64_t dv = dV + s * (C::kKVBytes >> 4);
+        const uint32_t tA = tP + (kc & 1) * 64, more = i > 0 ? 1u : 0u;
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kBlock / 16; ++kk) {
-            const uint64_t bd = sdesc_sw128(ring_a + s * C::kKVBytes + kk * 16 * 128, C::kKVChunkBytes, 1024);
-            tc_mma_ts(tO, tP + (kc & 1) * 64 + kk * 8, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            tc_mma_ts(tO, tA + kk * 8, dv + kk * (16 * 128 >> 4), kIdescPV, kk > 0 ? 1u : more);
           tc_commit(&pv_done[2 * c + (kc & 1)]);
           tc_commit(&vempty[s]);
           mbar_arrive(&pv_done[2 * c + (kc & 1)]);      // passes on the piece's `special`, seen through vready
@@ -787,7 +798,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       }
       if (last) break;
     }
-    if (lane == 0) {                              // (bounded)
+    if (elect_one()) {                            // (bounded)
       tc_commit(drain);
       mbar_wait_drain(drain, 0u);
     }
