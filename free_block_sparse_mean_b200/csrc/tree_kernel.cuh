@@ -97,7 +97,7 @@ struct TreeCfg {
   static constexpr int oK = oQ + NC * kQBufs * kQBytes;
   static constexpr int oV = oK + ST * kKVBytes;
   static constexpr int oBar = oV + ST * kKVBytes;
-  static constexpr int kNumBars = 5 * ST + 2 * kPieces + NC * (2 * kQBufs + 6) + 1;
+  static constexpr int kNumBars = 6 * ST + 2 * kPieces + NC * (2 * kQBufs + 6) + 1;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int oPieces = oMisc + 16 * 4 + kThreads / 32 * 8;
   static constexpr int kSmemBytes = oPieces + kPieces * 48;
@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   uint64_t* kempty = kfull + C::ST;        // [ST] K stage consumed by every chain's S MMA
   uint64_t* vfull = kempty + C::ST;        // [ST] V stage loaded
   uint64_t* vempty = vfull + C::ST;        // [ST] V stage consumed by every chain's P.V MMA
-  uint64_t* vready = vempty + C::ST;       // [ST] V stage loaded and its unseen rows dealt with
-  uint64_t* piece_full = vready + C::ST;   // [kPieces] piece written
+  uint64_t* vready = vempty + C::ST;       // [ST] by number of such a block: what its V holds unseen is dealt with
+  uint64_t* vpart = vready + C::ST;        // [ST] by the same number: its V load was issued
+  uint64_t* piece_full = vpart + C::ST;   // [kPieces] piece written
   uint64_t* piece_empty = piece_full + C::kPieces;  // [kPieces] piece read by every other warp with a part in it
   uint64_t* q_full = piece_empty + C::kPieces;   // [NC][kQBufs] Q of a tile loaded
   uint64_t* q_empty = q_full + NC * C::kQBufs;  // [NC][kQBufs] the S MMAs of the Q's piece finished
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       mbar_init(&vfull[s], 1);
       mbar_init(&vempty[s], NC);
       mbar_init(&vready[s], 1);
+      mbar_init(&vpart[s], 1);
     }
     for (int b = 0; b < C::kPieces; ++b) {
       mbar_init(&piece_full[b], 1);
@@ -553,6 +555,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     __syncwarp();
     if (lane == 0) mbar_arrive(&piece_empty[item % C::kPieces]);
   };
+  // the first block of a piece from b0 on that reaches place `open`
+  auto first_part = [](int open, int b0) { return max(open / kBlock - b0, 0); };
   // the chain has rows in the piece
   auto active = [&](const TreePiece* p, int c) { return p->tile * a.TT + c * a.TC < p->T; };
 
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     ld.w = walk;
     ld.more = true;
     ld.open(a, lane);
-    int nk = 0, nv = 0, item = 0;                 // loads issued, pieces written
+    int nk = 0, nv = 0, item = 0, nw = 0;         // loads issued, pieces written, blocks seen in part
     while (ld.more) {
       const int s = nk % C::ST;
       const uint32_t before = static_cast<uint32_t>(nk / C::ST - 1) & 1u;
@@ -610,7 +614,13 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       ++nk;
       if (ld.k == 0) ++item;
       if (nk > C::ST && !warp_wait(&vempty[s], before, abort_flag)) break;
-      if (lane == 0) mbar_expect_tx(&vfull[s], bytes);
+      const bool part =
+          ld.k >= first_part(masked ? ld.w.q.L : ld.w.q.L + ld.w.tile * a.TT + 1, ld.w.b0);
+      if (lane == 0) {
+        mbar_expect_tx(&vfull[s], bytes);
+        if (part) mbar_arrive(&vpart[nw % C::ST]);
+      }
+      if (part) ++nw;
       __syncwarp();
       if (mine_loads)
         tma_load_5d(sV + s * C::kKVBytes + dst_off, &tmV, 0, at & (page - 1), my_chunk, ld.w.head, id, &vfull[s]);
@@ -628,7 +638,9 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   } else if (warp == 1) {
     // ------------------------------------------------------------ Q loads, what a V block holds unseen
     if (lane == 0) tma_prefetch_desc(&tmQ);
-    int k = 0, nq[NC] = {};                       // blocks of the share, Q tiles loaded of each chain
+    // Only blocks that some row does not see whole are waited for: a warp that waited for
+    // every V block as it came in slowed the softmax warps on its scheduler by a third.
+    int k = 0, nw = 0, nq[NC] = {};               // blocks of the share, of them seen in part, Q tiles of each chain
     bool ok = true;
     for (int item = 0; ok; ++item) {
       TreePiece* p = piece(item);
@@ -655,48 +667,49 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       const int keys = p->L + p->T, n = p->n, b0 = p->b0, last = p->last;
       // every row of the tile sees the keys before `open`; from there on rows differ
       const int open = masked ? p->L : p->L + p->tile * a.TT + 1;
-      for (int i = 0; ok && i < n; ++i, ++k) {
-        const int s = k % C::ST;
-        if (!warp_wait(&vfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag)) {
+      for (int i = first_part(open, b0); ok && i < n; ++i, ++nw) {
+        const int s = (k + i) % C::ST;
+        // (vpart first: the block's phase of vfull has begun)
+        if (!warp_wait(&vpart[nw % C::ST], static_cast<uint32_t>(nw / C::ST) & 1u, abort_flag) ||
+            !warp_wait(&vfull[s], static_cast<uint32_t>((k + i) / C::ST) & 1u, abort_flag)) {
           ok = false;
           break;
         }
         const int kb = (b0 + i) * kBlock;
-        if (kb + kBlock > open) {
-          // rows behind the last token to zero; elements that are not finite out of
-          // the rows that not every query sees
-          const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
-          bool taken_out = false;
-          uint8_t* v = sV + s * C::kKVBytes;
-          for (int h = 0; h < C::kChunks; ++h) {
-            for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
-              uint4* at = reinterpret_cast<uint4*>(v + h * C::kKVChunkBytes + x * 16);
-              if (x >= live * 8) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                uint4 w = *at;
-                uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-                bool any = false;
+        // rows behind the last token to zero; elements that are not finite out of
+        // the rows that not every query sees
+        const int live = min(kBlock, keys - kb), seen = max(0, min(open - kb, live));
+        bool taken_out = false;
+        uint8_t* v = sV + s * C::kKVBytes;
+        for (int h = 0; h < C::kChunks; ++h) {
+          for (int x = seen * 8 + lane; x < kBlock * 8; x += 32) {     // 16-byte pieces, 8 a row
+            uint4* at = reinterpret_cast<uint4*>(v + h * C::kKVChunkBytes + x * 16);
+            if (x >= live * 8) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint4 w = *at;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+              bool any = false;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const bool lo = not_finite16<kElem>(e[u]), hi = not_finite16<kElem>(e[u] >> 16);
-                  if (lo) e[u] &= 0xffff0000u;
-                  if (hi) e[u] &= 0x0000ffffu;
-                  any |= lo | hi;
-                }
-                if (any) {
-                  *at = w;
-                  taken_out = true;
-                }
+              for (int u = 0; u < 4; ++u) {
+                const bool lo = not_finite16<kElem>(e[u]), hi = not_finite16<kElem>(e[u] >> 16);
+                if (lo) e[u] &= 0xffff0000u;
+                if (hi) e[u] &= 0x0000ffffu;
+                any |= lo | hi;
+              }
+              if (any) {
+                *at = w;
+                taken_out = true;
               }
             }
           }
-          fence_proxy_async_smem();
-          if (__any_sync(FULL, taken_out) && lane == 0) p->special = 1;
-          __syncwarp();
         }
-        if (lane == 0) mbar_arrive(&vready[s]);
+        fence_proxy_async_smem();
+        if (__any_sync(FULL, taken_out) && lane == 0) p->special = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vready[nw % C::ST]);
       }
+      k += n;
       release(item);
       if (last) break;
     }
@@ -763,17 +776,23 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     const int c = warp - 2 - NC;
     const uint32_t tP = tmem_base + c * C::kChainCols + C::kColS, tO = tmem_base + c * C::kChainCols + C::kColO;
     const uint64_t dV = sdesc_sw128(smem_u32(sV), C::kKVChunkBytes, 1024);
-    int k = 0, kc = 0;                            // blocks of the share, of the chain
+    int k = 0, kc = 0, nw = 0;                    // blocks of the share, of the chain, of those seen in part
     bool ok = true;
     for (int item = 0; ok; ++item) {
       const TreePiece* p = piece(item);
       if (!p) break;
       const bool act = active(p, c);
       const int n = p->n, last = p->last;
+      const int part = first_part(masked ? p->L : p->L + p->tile * a.TT + 1, p->b0);
       release(item);
       for (int i = 0; i < n; ++i, ++k) {
         const int s = k % C::ST;
-        if (!warp_wait(&vready[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag) ||
+        bool ready = warp_wait(&vfull[s], static_cast<uint32_t>(k / C::ST) & 1u, abort_flag);
+        if (ready && i >= part) {
+          ready = warp_wait(&vready[nw % C::ST], static_cast<uint32_t>(nw / C::ST) & 1u, abort_flag);
+          ++nw;
+        }
+        if (!ready ||
             (act && !warp_wait(&p_full[2 * c + (kc & 1)], static_cast<uint32_t>(kc >> 1) & 1u, abort_flag))) {
           ok = false;
           break;
