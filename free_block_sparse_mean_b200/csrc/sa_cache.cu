@@ -112,7 +112,7 @@ struct TreeLayout {
   int G, TC, chains;          // query heads of a key head, tokens of a chain, chains of a CTA
   int ctas;                   // CTAs that share the call's key blocks
   bool split;                 // the border between two CTAs' shares may cut a tile
-  size_t part_o, part_ml, line, total;
+  size_t part_o, part_ml, cut, total;
 };
 TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -127,7 +127,7 @@ TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
   size_t o = 0;
   L.part_o = o; o += al(rows * c.d * sizeof(float));
   L.part_ml = o; o += al(rows * sizeof(float2));
-  L.line = o; o += L.split ? al((static_cast<size_t>(s.R) + 2) * sizeof(long long)) : 0;
+  L.cut = o; o += L.split ? al(L.ctas * sizeof(int4)) : 0;
   L.total = o;
   return L;
 }
@@ -142,9 +142,18 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                                                        c.token_stride, c.head_stride);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   if (L.split) {
-    const int64_t warps = static_cast<int64_t>(a.n) * a.Hkv * a.G;
-    sa::tree_combine_kernel<D, kElem><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+    // a block for each row of a small tile, for eight of a large one
+    const int rows = a.TT * a.G, per = rows <= 32 ? 1 : 8;
+    cudaLaunchAttribute early{};                  // its blocks come in as those of the first kernel leave
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(L.ctas, (rows + per - 1) / per);
+    cfg.blockDim = dim3(32 * sa::kCombineWarps);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, sa::tree_combine_kernel<D, kElem>, a, per) != cudaSuccess) return SA_ERR_CUDA;
   }
   return SA_OK;
 }
@@ -313,7 +322,7 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   if (L.split) {
     a.part_o = reinterpret_cast<float*>(ws + L.part_o);
     a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
-    a.line = reinterpret_cast<long long*>(ws + L.line);
+    a.cut = reinterpret_cast<int4*>(ws + L.cut);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool small = L.TC * L.G <= 32, f16 = c.dtype == SA_F16;
