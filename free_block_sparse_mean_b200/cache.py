@@ -63,71 +63,86 @@ class CachePlan:
     max_new: int = 0
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream(dev) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _call(name: str, status: int):
-    if status != _lib.SA_OK:
-        raise SparseAttnError(name, status, _lib.load())
+def _launch(name: str, dev, call, *args):
+    """The C call on the device's current torch stream. A step of small requests costs its
+    calls, not its kernels (4 us of 37 for a plan of 64 requests), so nothing here is
+    done that the case does not need: no device switch on the current device, no views."""
+    if _get_device() == dev.index:
+        st = call(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, _raw_stream(dev.index))
+    if st != _lib.SA_OK:
+        raise SparseAttnError(name, st, _lib.load())
 
 
 def _ints(name: str, t: torch.Tensor, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() \
-            or tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or t.device != dev \
+            or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {dev}")
 
 
 def _rows(name: str, t: torch.Tensor, dtype, dev):
-    if t.dim() != 3 or t.dtype != dtype or t.device != dev:
+    if t.dim() != 3 or t.dtype is not dtype or t.device != dev:
         raise ValueError(f"{name} must be [n, heads, d] in the cache's type on its device")
     _strides(name, t)
 
 
 def _strides(name: str, t: torch.Tensor):
     """d contiguous, every other step a positive multiple of 8 elements, 16-byte base."""
-    if t.stride(-1) != 1 or any(s <= 0 or s % 8 for s, e in zip(t.stride()[:-1], t.shape[:-1]) if e > 1) \
-            or t.data_ptr() % 16:
+    good = t.data_ptr() % 16 == 0
+    if good and not (t.is_contiguous() and t.shape[-1] % 8 == 0):
+        st = t.stride()
+        good = st[-1] == 1 and all(s > 0 and s % 8 == 0 for s, e in zip(st[:-1], t.shape) if e > 1)
+    if not good:
         raise ValueError(f"{name} must have a contiguous last dimension, strides that are positive multiples of 8 "
                          "elements and a 16-byte aligned base")
 
 
+def _same_layout(a: torch.Tensor, b: torch.Tensor) -> bool:
+    x, y = a.stride(), b.stride()
+    return x == y or all(i == j for i, j, e in zip(x, y, a.shape) if e > 1)
+
+
 def _cache(k: torch.Tensor, v: torch.Tensor, dims: int = 4) -> SaCache:
-    if not k.is_cuda or k.dtype not in _DTYPES:
+    dtype = _DTYPES.get(k.dtype)
+    if dtype is None or not k.is_cuda:
         raise ValueError("a cache must be a bf16 or fp16 CUDA tensor")
-    if k.dim() != dims or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device \
-            or any(a != b for a, b, e in zip(k.stride(), v.stride(), k.shape) if e > 1):
+    shape = k.shape
+    if len(shape) != dims or v.shape != shape or v.dtype is not k.dtype or v.device != k.device \
+            or not _same_layout(k, v):
         raise ValueError("the caches must be [pages, page_size, Hkv, d] of one type, shape and layout")
     if k.numel() == 0:
         raise ValueError("the caches must not be empty")
     _strides("the cache", k)
     _strides("the cache", v)
-    pages, page, heads, d = k.shape[-4:]
-    ps, ts, hs = k.stride()[-4:-1]
-    if pages == 1:
-        ps = page * heads * d
-    return SaCache(pages, page, heads, d, _DTYPES[k.dtype], ps, ts, hs if heads > 1 else d)
+    pages, page, heads, d = shape[-4:]
+    ps, ts, hs, _ = k.stride()[-4:]
+    return SaCache(pages, page, heads, d, dtype, ps if pages > 1 else page * heads * d, ts, hs if heads > 1 else d)
 
 
 def _step(plan: CachePlan, n: int, dev, masked: bool = True) -> SaStep:
-    if plan.table.dim() != 2:
+    table, lens, starts, granted = plan.table, plan.lens, plan.starts, plan.granted
+    if table.dim() != 2:
         raise ValueError("the plan's table must be [R, width]")
-    R, width = plan.table.shape
-    _ints("the plan's table", plan.table, (R, width), dev)
-    _ints("the plan's lens", plan.lens, (R,), dev)
-    _ints("the plan's starts", plan.starts, (R + 1,), dev)
-    if plan.granted is not None:
-        _ints("the plan's granted", plan.granted, (R,), dev)
+    R, width = shape = table.shape
+    _ints("the plan's table", table, shape, dev)
+    _ints("the plan's lens", lens, (R,), dev)
+    _ints("the plan's starts", starts, (R + 1,), dev)
+    if granted is not None:
+        _ints("the plan's granted", granted, (R,), dev)
+        granted = granted.data_ptr()
     words, mask = 0, None
     if masked and plan.mask is not None:
-        words, mask = plan.mask.shape[-1], plan.mask
-        _ints("the plan's mask", mask, (n, words), dev)
-    return SaStep(R, n, width, int(plan.max_new), words, _ptr(plan.starts), _ptr(plan.lens), _ptr(plan.granted),
-                  _ptr(plan.table), _ptr(mask))
+        words = plan.mask.shape[-1]
+        _ints("the plan's mask", plan.mask, (n, words), dev)
+        mask = plan.mask.data_ptr()
+    return SaStep(R, n, width, int(plan.max_new), words, starts.data_ptr(), lens.data_ptr(), granted, table.data_ptr(),
+                  mask)
 
 
 def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: torch.Tensor, held: torch.Tensor,
@@ -149,8 +164,8 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
     if not lens.is_cuda or table.dim() != 2:
         raise ValueError("lens must be a CUDA tensor, table [R, width]")
     dev = lens.device
-    R, width = table.shape
-    _ints("table", table, (R, width), dev)
+    R, width = shape = table.shape
+    _ints("table", table, shape, dev)
     for name, t in (("lens", lens), ("new_tokens", new_tokens), ("held", held)):
         _ints(name, t, (R,), dev)
     _ints("nfree", nfree, (1,), dev)
@@ -165,10 +180,11 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
             raise ValueError("parents needs mask_words")
         _ints("parents", parents, (n,), dev)
     if out is None:
-        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
-        out = CachePlan(table=table, lens=lens, starts=new(R + 1), granted=new(R),
-                        mask=new(n, mask_words) if mask_words else None, slots=new(n), positions=new(n),
-                        held=new(R), nfree=new(1), free_pages=free_pages, max_new=int(max_new))
+        sizes = [R + 1, R, R, 1, n, n, n * mask_words]     # one buffer: an allocation costs more than a view
+        starts, granted, held_out, nfree_out, slots, positions, mask = \
+            torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
+        out = CachePlan(table, lens, starts, granted, mask.view(n, mask_words) if mask_words else None, slots,
+                        positions, held_out, nfree_out, free_pages, int(max_new))
     else:
         for name, t, shape in (("starts", out.starts, (R + 1,)), ("granted", out.granted, (R,)),
                                ("slots", out.slots, (n,)), ("positions", out.positions, (n,)),
@@ -179,13 +195,11 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
         else:
             out.mask = None
         out.table, out.lens, out.free_pages, out.max_new = table, lens, free_pages, int(max_new)
-    with torch.cuda.device(dev):
-        st = lib.sparse_attn_cache_plan(_ptr(lens), _ptr(new_tokens), _ptr(held), _ptr(nfree), _ptr(free_pages),
-                                        _ptr(table), _ptr(parents), R, free_pages.numel(), int(page_size), width, n,
-                                        mask_words, _ptr(out.held), _ptr(out.nfree), _ptr(out.starts),
-                                        _ptr(out.granted), _ptr(out.slots), _ptr(out.positions), _ptr(out.mask),
-                                        _stream(dev))
-    _call("sparse_attn_cache_plan", st)
+    _launch("sparse_attn_cache_plan", dev, lib.sparse_attn_cache_plan, lens.data_ptr(), new_tokens.data_ptr(),
+            held.data_ptr(), nfree.data_ptr(), free_pages.data_ptr(), table.data_ptr(),
+            None if parents is None else parents.data_ptr(), R, free_pages.shape[0], int(page_size), width, n, mask_words,
+            out.held.data_ptr(), out.nfree.data_ptr(), out.starts.data_ptr(), out.granted.data_ptr(),
+            out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if mask_words else None)
     return out
 
 
@@ -200,17 +214,15 @@ def sparse_attn_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tenso
     _rows("k", k, k_cache.dtype, dev)
     _rows("v", v, k_cache.dtype, dev)
     n = k.shape[0]
-    if tuple(k.shape[1:]) != (c.Hkv, c.d) or v.shape != k.shape:
+    if k.shape[1:] != (c.Hkv, c.d) or v.shape != k.shape:
         raise ValueError(f"k and v must be [n, {c.Hkv}, {c.d}]")
-    if any(a != b for a, b, e in zip(k.stride(), v.stride(), k.shape) if e > 1):
+    if not _same_layout(k, v):
         raise ValueError("k and v must have the same strides")
     _ints("slots", slots, (n,), dev)
     if n == 0:
         return
-    with torch.cuda.device(dev):
-        st = lib.sparse_attn_cache_write(_ptr(k), _ptr(v), k.stride(0), k.stride(1), n, _ptr(slots), _ptr(k_cache),
-                                         _ptr(v_cache), c, _stream(dev))
-    _call("sparse_attn_cache_write", st)
+    _launch("sparse_attn_cache_write", dev, lib.sparse_attn_cache_write, k.data_ptr(), v.data_ptr(), k.stride(0),
+            k.stride(1), n, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), c)
 
 
 def sparse_attn_tree_workspace_size(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -253,16 +265,14 @@ def sparse_attn_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         return out
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    ws_bytes = int(lib.sparse_attn_tree_workspace_size(c, s, Hq))
     if workspace is None:
-        workspace = torch.empty((max(ws_bytes, 256),), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(int(lib.sparse_attn_tree_workspace_size(c, s, Hq)), dtype=torch.uint8, device=dev)
     elif workspace.device != dev:
         raise ValueError("workspace must be on q's device")
-    with torch.cuda.device(dev):
-        st = lib.sparse_attn_tree_fwd(_ptr(q), q.stride(0), q.stride(1), Hq, _ptr(k_cache), _ptr(v_cache), c, s,
-                                      float(scale), _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
-                                      _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
-    _call("sparse_attn_tree_fwd", st)
+    _launch("sparse_attn_tree_fwd", dev, lib.sparse_attn_tree_fwd, q.data_ptr(), q.stride(0), q.stride(1), Hq,
+            k_cache.data_ptr(), v_cache.data_ptr(), c, s, float(scale), out.data_ptr(), out.stride(0), out.stride(1),
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return out
 
 
@@ -284,7 +294,5 @@ def sparse_attn_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, plan:
         raise ValueError("accepted must be [R, cols]")
     _ints("accepted", accepted, (s.R, accepted.shape[1]), dev)
     _ints("taken", taken, (s.R,), dev)
-    with torch.cuda.device(dev):
-        st = lib.sparse_attn_cache_accept(_ptr(k_cache), _ptr(v_cache), c, layers, layer_stride, s, _ptr(accepted),
-                                          accepted.shape[1], _ptr(taken), _stream(dev))
-    _call("sparse_attn_cache_accept", st)
+    _launch("sparse_attn_cache_accept", dev, lib.sparse_attn_cache_accept, k_cache.data_ptr(), v_cache.data_ptr(), c,
+            layers, layer_stride, s, accepted.data_ptr(), accepted.shape[1], taken.data_ptr())
