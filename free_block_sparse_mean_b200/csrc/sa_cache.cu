@@ -18,7 +18,7 @@
 namespace {
 
 constexpr int kSMs = 148;                       // B200
-constexpr int kTreeMinBlocks = 2;               // smallest share of a CTA, in 64-key blocks
+constexpr int kTreeMinCost = 3;                 // smallest share of a CTA, in 64-key blocks
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
@@ -138,21 +138,27 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   using Cfg = sa::TreeCfg<D, NC, kSmallQ>;
   auto kern = sa::tree_fwd_kernel<D, kElem, NC, kSmallQ>;
   if (sa::set_smem(kern, Cfg::kSmemBytes) != SA_OK) return SA_ERR_CUDA;
-  kern<<<L.ctas, Cfg::kThreads, Cfg::kSmemBytes, st>>>(mq, mk, mv, a, static_cast<const uint16_t*>(V), c.page_stride,
-                                                       c.token_stride, c.head_stride);
-  if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+  // each kernel sets itself up while the one before it in the stream ends, and waits for that itself
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(L.ctas);
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a, static_cast<const uint16_t*>(V),
+                         static_cast<long long>(c.page_stride), static_cast<long long>(c.token_stride),
+                         static_cast<long long>(c.head_stride)) != cudaSuccess)
+    return SA_ERR_CUDA;
   if (L.split) {
     // a block for each row of a small tile, for eight of a large one
     const int rows = a.TT * a.G, per = rows <= 32 ? 1 : 8;
-    cudaLaunchAttribute early{};                  // its blocks come in as those of the first kernel leave
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(L.ctas, (rows + per - 1) / per);
     cfg.blockDim = dim3(32 * sa::kCombineWarps);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, sa::tree_combine_kernel<D, kElem>, a, per) != cudaSuccess) return SA_ERR_CUDA;
   }
   return SA_OK;
@@ -313,7 +319,7 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   a.G = L.G;
   a.TT = L.chains * L.TC;
   a.TC = L.TC;
-  a.min_blocks = kTreeMinBlocks;
+  a.min_cost = kTreeMinCost;
   a.O = O;
   a.o_token = s.n > 1 ? o_token : 0;
   a.o_head = Hq > 1 ? o_head : 0;

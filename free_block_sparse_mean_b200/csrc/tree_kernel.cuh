@@ -110,7 +110,7 @@ struct TreeArgs {
   const uint32_t* mask;           // [n][words] or null
   int R, n, width, pages, page_shift, words;
   int Hkv, G, TT, TC;             // key heads, query heads each, tokens of a tile, of a chain's part of it
-  int min_blocks;                 // smallest share of a CTA, in blocks
+  int min_cost;                   // smallest share of a CTA
   void* O;
   long long o_token, o_head;      // strides in elements
   float* lse;                     // [n][Hkv * G] or null
@@ -152,18 +152,25 @@ __device__ __forceinline__ int tree_tile_blocks(const TreeReq& q, int tile, int 
   return masked ? q.nb : (q.L + min(q.T, (tile + 1) * TT) + kBlock - 1) / kBlock;
 }
 
+// a / b for a >= 0, b > 0: 64-bit division is a long subroutine, and hardly ever needed.
+__device__ __forceinline__ long long div64(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // sum of floor((a i + b) / m) over i = 0 .. n-1 (a, b >= 0, m > 0), by the Euclidean
 // reduction: take whole parts out of a and b, then count the lattice points the other way.
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long sum = 0;
   while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
+    const long long qa = div64(a, m), qb = div64(b, m);
+    sum += (n - 1) * n / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
     const long long y = a * n + b;
     if (y < m) break;
-    n = y / m;
-    b = y % m;
+    n = div64(y, m);
+    b = y - n * m;
     const long long t = m;
     m = a;
     a = t;
@@ -171,20 +178,30 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
   return sum;
 }
 
-// Blocks of a key head's first `tiles` tiles of a request.
-__device__ __forceinline__ long long tree_blocks_before(const TreeReq& q, int tiles, int TT, bool masked) {
+// What a tile costs beside its blocks, in blocks: Q's load, the pass of O out of TMEM.
+// Without it 64 ragged requests of up to 1,000 tokens (512 tiles of 1 to 16 blocks) took
+// their CTAs between 22 and 42 us.
+constexpr int kTileCost = 2;
+
+// Cost of a key head's first `tiles` tiles of a request: their blocks and kTileCost each.
+__device__ __forceinline__ long long tree_cost_before(const TreeReq& q, int tiles, int TT, bool masked) {
   if (tiles <= 0) return 0;
-  if (masked) return static_cast<long long>(tiles) * q.nb;
+  const long long own = static_cast<long long>(tiles) * kTileCost;
+  if (masked) return static_cast<long long>(tiles) * q.nb + own;
   const int full = min(tiles, q.tiles - 1);            // the last tile may hold fewer tokens
   const long long s = full > 0 ? floor_sum(full, kBlock, TT, q.L + TT + kBlock - 1) : 0;
-  return tiles == q.tiles ? s + q.nb : s;
+  return (tiles == q.tiles ? s + q.nb : s) + own;
 }
 
-// The share of the line that CTA c of `ctas` takes begins here.
-__device__ __forceinline__ long long tree_share(long long total, int c, int ctas) { return total * c / ctas; }
-// The CTA whose share holds block x of the line.
+// The share of the line that CTA c of `ctas` takes begins here: floor(total * c / ctas).
+__device__ __forceinline__ long long tree_share(long long total, int c, int ctas) {
+  const long long q = div64(total, ctas);
+  const int rest = static_cast<int>(total - q * ctas);
+  return q * c + rest * c / ctas;
+}
+// The CTA whose share holds place x of the line.
 __device__ __forceinline__ int tree_owner(long long total, long long x, int ctas) {
-  return static_cast<int>(((x + 1) * ctas + total - 1) / total) - 1;
+  return static_cast<int>(div64((x + 1) * ctas + total - 1, total)) - 1;
 }
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v,
@@ -279,22 +296,34 @@ __device__ __forceinline__ void tree_exp32(const float (&s)[32], float sc, float
 // is its blocks [b0, b0 + n). A piece that begins inside its tile is kept for the end, so
 // that every CTA begins with block 0 of some tile: the CTAs on one key head then read the
 // same keys at about the same time, from L2. In the line's order a prompt's chunk (2 x
-// 2,048 tokens behind 30,000, 8 key heads) took 1,622 us, DRAM bound at 9 GB a call.
+// 2,048 tokens behind 30,000, 8 key heads) took 1,622 us, DRAM bound at 9 GB a call,
+// against 1,410 (the kernel's first form).
 struct TreeWalk {
   int r, head, tile, b0, n, nbt;
   TreeReq q;
-  long long left;                 // blocks of the share from this piece on, the kept piece aside
+  long long left;                 // the share's cost from this piece on, the kept piece aside
   int kr, khead, ktile, kb0;      // the kept piece (kr = -1: none)
 
   __device__ __forceinline__ void cut(const TreeArgs& a) {
     nbt = tree_tile_blocks(q, tile, a.TT, a.mask != nullptr);
     n = static_cast<int>(min(left, static_cast<long long>(nbt - b0)));
   }
-  // The first piece, from the share's first block (r, head, tile, b0, q and left set).
-  __device__ __forceinline__ void begin(const TreeArgs& a) {
-    cut(a);
+  __device__ __forceinline__ long long after() const { return left - n - (b0 + n == nbt ? kTileCost : 0); }
+  __device__ __forceinline__ bool last() const { return after() <= 0 && kr < 0; }
+  // The first piece, from the share's first place: `at` in its tile (r, head, tile, q and
+  // left set). False if the share holds no block.
+  __device__ __forceinline__ bool begin(const TreeArgs& a, int at) {
     kr = -1;
-    if (b0 > 0 && n < left) {
+    nbt = tree_tile_blocks(q, tile, a.TT, a.mask != nullptr);
+    if (at >= nbt) {                        // the share begins in what the tile costs beside its blocks
+      b0 = nbt;
+      n = 0;
+      left += at - nbt;
+      return next(a);
+    }
+    b0 = at;
+    cut(a);
+    if (b0 > 0 && after() > 0) {
       const int first = r;
       khead = head;
       ktile = tile;
@@ -302,10 +331,11 @@ struct TreeWalk {
       next(a);
       kr = first;
     }
+    return true;
   }
   // To the next piece of the share; false at its end.
   __device__ __forceinline__ bool next(const TreeArgs& a) {
-    left -= n;
+    left = after();
     bool bad;
     if (left <= 0) {
       if (kr < 0) return false;
@@ -420,114 +450,83 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   const int warp = __shfl_sync(FULL, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   // ------------------------------------------------------------ set up, find this CTA's share
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::ST; ++s) {
-      mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], NC);
-      mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], NC);
-      mbar_init(&vready[s], 1);
-      mbar_init(&vpart[s], 1);
-    }
-    for (int b = 0; b < C::kPieces; ++b) {
-      mbar_init(&piece_full[b], 1);
-      mbar_init(&piece_empty[b], 1 + 6 * NC);
-    }
-    for (int b = 0; b < NC * C::kQBufs; ++b) {
-      mbar_init(&q_full[b], 1);
-      mbar_init(&q_empty[b], 1);
-    }
-    for (int b = 0; b < 2 * NC; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 4);
-      mbar_init(&pv_done[b], 2);
-    }
-    mbar_init(drain, 2 * NC);
+  if (threadIdx.x < C::kNumBars) {
+    uint64_t* bar = bars + threadIdx.x;
+    int count = 1;
+    if ((bar >= kempty && bar < vfull) || (bar >= vempty && bar < vready)) count = NC;
+    if (bar >= piece_empty && bar < q_full) count = 1 + 6 * NC;
+    if (bar >= p_full && bar < pv_done) count = 4;
+    if (bar >= pv_done && bar < drain) count = 2;
+    if (bar == drain) count = 2 * NC;
+    mbar_init(bar, count);
     fence_mbar_init();
-    *abort_flag = 0;
-    found[0] = -1;
   }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  // what is before in the stream has finished; what is behind may set itself up
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int cta = static_cast<int>(blockIdx.x);
   bool bad = false;
   const bool masked = a.mask != nullptr;
   TreeReq mine{0, 0, 0, 0};
-  long long blocks = 0, total = 0;            // of the thread's request, of all
-  for (int r = threadIdx.x; r < a.R; r += C::kThreads) {
-    mine = tree_request(a, r, &bad);
-    blocks = tree_blocks_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
-    total += blocks;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(FULL, total, o);
-  if (lane == 0) wsum[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += wsum[w];
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + a.min_blocks - 1) / a.min_blocks));
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0 && a.cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (blockIdx.x == 0 && bad) atomicOr(&g_dev_error, DEVERR_VALUE);
-  const int cta = static_cast<int>(blockIdx.x);
-  if (cta >= max(ctas, 1)) return;
-  const long long share0 = ctas > 0 ? tree_share(total, cta, ctas) : 0;
-  const long long share1 = ctas > 0 ? tree_share(total, cta + 1, ctas) : 0;
-  __syncthreads();
-  long long before = 0;
-  for (int r0 = 0; r0 < a.R; r0 += C::kThreads) {
-    const int r = r0 + threadIdx.x;
-    if (a.R > C::kThreads) {
-      bool again;
-      mine = r < a.R ? tree_request(a, r, &again) : TreeReq{0, 0, 0, 0};
-      blocks = r < a.R ? tree_blocks_before(mine, mine.tiles, a.TT, masked) * a.Hkv : 0;
-    }
-    long long upto = blocks;
+  long long cost = 0, upto = 0, total = 0;    // of the thread's request, of the requests up to it, of all
+  auto scan = [&](long long v) {              // inclusive over the CTA; `total` grows by the sum
+    const long long before = total;
+    upto = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(FULL, upto, o);
       if (lane >= o) upto += x;
     }
+    __syncthreads();
     if (lane == 31) wsum[warp] = upto;
     __syncthreads();
     upto += before;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) upto += wsum[w];
-      before += wsum[w];
+      total += wsum[w];
     }
-    const long long at = upto - blocks;
-    if (blocks > 0 && share0 >= at && share0 < upto) {
+  };
+  for (int r0 = 0; r0 < a.R; r0 += C::kThreads) {
+    const int r = r0 + threadIdx.x;
+    cost = 0;
+    if (r < a.R) {
+      mine = tree_request(a, r, &bad);
+      cost = tree_cost_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
+    }
+    scan(cost);
+  }
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), div64(total + a.min_cost - 1, a.min_cost)));
+  if (threadIdx.x == 0 && a.cut) a.cut[cta] = make_int4(0, 0, 0, 0);
+  if (cta == 0 && bad) atomicOr(&g_dev_error, DEVERR_VALUE);
+  if (cta >= ctas) return;
+  const long long all = total, share0 = tree_share(all, cta, ctas), share1 = tree_share(all, cta + 1, ctas);
+  if (warp == 1) tmem_alloc(tmem_holder, NC * C::kChainCols);
+  auto find = [&](int r) {                    // the share's first place lies in the thread's request
+    if (cost > 0 && share0 >= upto - cost && share0 < upto) {
       found[0] = r;
       found[1] = mine.T;
       found[2] = mine.L;
-      *found_at = at;
+      *found_at = upto - cost;
     }
-    __syncthreads();
-    if (found[0] >= 0) break;
-  }
-  if (found[0] < 0) return;                   // no work at all
-  TreeWalk walk;
-  walk.r = found[0];
-  walk.q.T = found[1];
-  walk.q.L = found[2];
-  walk.q.nb = (walk.q.L + walk.q.T + kBlock - 1) / kBlock;
-  walk.q.tiles = (walk.q.T + a.TT - 1) / a.TT;
-  walk.left = share1 - share0;
-  {
-    const long long per_head = tree_blocks_before(walk.q, walk.q.tiles, a.TT, masked);
-    long long x = share0 - *found_at;
-    walk.head = static_cast<int>(x / per_head);
-    x -= walk.head * per_head;
-    int lo = 0, hi = walk.q.tiles;            // the last tile that begins at or before x
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tree_blocks_before(walk.q, mid, a.TT, masked) <= x)
-        lo = mid;
-      else
-        hi = mid;
+  };
+  if (a.R <= C::kThreads) {
+    find(threadIdx.x);
+  } else {
+    total = 0;
+    for (int r0 = 0; r0 < a.R; r0 += C::kThreads) {
+      const int r = r0 + threadIdx.x;
+      bool again;
+      cost = 0;
+      if (r < a.R) {
+        mine = tree_request(a, r, &again);
+        cost = tree_cost_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
+      }
+      scan(cost);
+      find(r);
+      if (share0 < total) break;
     }
-    walk.tile = lo;
-    walk.b0 = static_cast<int>(x - tree_blocks_before(walk.q, lo, a.TT, masked));
-    walk.begin(a);
   }
   const int page = 1 << a.page_shift;
   // a block is 64 / sub boxes of `sub` tokens; below 64 tokens a box holds one
@@ -538,7 +537,6 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   const bool loads = subs == 1 ? lane == 0 : my_chunk < C::kChunks;
   const int sub_off = my_sub * sub, dst_off = my_chunk * C::kKVChunkBytes + sub_off * 128;
 
-  if (warp == 1) tmem_alloc(tmem_holder, NC * C::kChainCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -568,10 +566,37 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     }
     bool bad_page = false;
     TreeLoad ld;
-    ld.w = walk;
-    ld.more = true;
-    ld.open(a, lane);
-    int nk = 0, nv = 0, item = 0, nw = 0;         // loads issued, pieces written, blocks seen in part
+    {
+      TreeWalk& w = ld.w;
+      w.r = found[0];
+      w.q.T = found[1];
+      w.q.L = found[2];
+      w.q.nb = (w.q.L + w.q.T + kBlock - 1) / kBlock;
+      w.q.tiles = (w.q.T + a.TT - 1) / a.TT;
+      w.left = share1 - share0;
+      const long long per_head = tree_cost_before(w.q, w.q.tiles, a.TT, masked);
+      long long x = share0 - *found_at;
+      w.head = static_cast<int>(div64(x, per_head));
+      x -= w.head * per_head;
+      int lo = 0, hi = w.q.tiles;             // the last tile that begins at or before x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tree_cost_before(w.q, mid, a.TT, masked) <= x)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      w.tile = lo;
+      ld.more = w.begin(a, static_cast<int>(x - tree_cost_before(w.q, lo, a.TT, masked)));
+    }
+    if (ld.more) {
+      ld.open(a, lane);
+    } else if (lane == 0) {                   // no block at all: an empty piece for the others
+      pieces[0] = TreePiece{};
+      pieces[0].last = 1;
+      mbar_arrive(&piece_full[0]);
+    }
+    int nk = 0, nv = 0, item = 0, nw = 0;     // loads issued, pieces written, blocks seen in part
     while (ld.more) {
       const int s = nk % C::ST;
       const uint32_t before = static_cast<uint32_t>(nk / C::ST - 1) & 1u;
@@ -601,11 +626,11 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
           p->b0 = ld.w.b0;
           p->n = ld.w.n;
           p->nbt = ld.w.nbt;
-          p->last = ld.w.left == ld.w.n && ld.w.kr < 0;
+          p->last = ld.w.last();
           p->special = 0;
           if (ld.w.b0 == 0 && ld.w.n < ld.w.nbt)       // (its blocks are the share's last)
             a.cut[cta] = make_int4(p->tok0 + p->tile * a.TT, min(a.TT, p->T - p->tile * a.TT) * a.G, p->head,
-                                   tree_owner(total, share1 - p->n + p->nbt - 1, ctas));
+                                   tree_owner(all, share1 - p->n + p->nbt - 1, ctas));
           mbar_arrive(&piece_full[item % C::kPieces]);
         }
       }
@@ -958,12 +983,13 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       const long long token = static_cast<long long>(p->tok0) + t;
       const long long prow = (2LL * cta + (b0 == 0 ? 1 : 0)) * (a.TT * a.G) + c * a.TC * a.G + row;
       uint16_t* orow = static_cast<uint16_t*>(a.O) + token * a.o_token + hq * a.o_head;
-#pragma unroll 1
+      tmem_ld32(o_addr, s0);
+#pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
-        float o[32];
-        tmem_ld32(o_addr + cc, o);
+        float(&o)[32] = (cc & 32) ? s1 : s0;
         tmem_wait_ld();
         pin32(o);
+        if (cc + 32 < D) tmem_ld32(o_addr + cc + 32, (cc & 32) ? s0 : s1);   // comes in under this one's stores
         if (valid) {
           if (l == 0.f) {
 #pragma unroll
@@ -1040,10 +1066,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     tree_combine_kernel(const __grid_constant__ TreeArgs a, int rows_per_block) {
   constexpr int kPer = D / 32;                      // elements of a lane
   __shared__ float s_o[kCombineWarps][D];
-  __shared__ float s_l[kCombineWarps];
-  const unsigned FULL = 0xffffffffu;
+  __shared__ float2 s_ml[kCombineWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const int c0 = static_cast<int>(blockIdx.x);
   const int4 tile = a.cut[c0];
   const int row0 = static_cast<int>(blockIdx.y) * rows_per_block, row1 = min(row0 + rows_per_block, tile.y);
@@ -1053,36 +1079,47 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   const int step = shared ? kCombineWarps : 1;
   for (int row = shared ? row0 : row0 + warp; row < row1; row += shared ? 1 : kCombineWarps) {
     auto at = [&](int p) { return (2LL * (c0 + p) + (p == 0 ? 1 : 0)) * (a.TT * a.G) + row; };
-    float m = -INFINITY;
-    for (int p = lane; p < np; p += 32) m = fmaxf(m, a.part_ml[at(p)].x);
+    float m = -INFINITY, l = 0.f, acc[kPer] = {};
+    auto add = [&](float m1, float l1, const float (&v)[kPer]) {   // one more piece
+      const float top = fmaxf(m, m1), ref = top == -INFINITY ? 0.f : top;
+      const float w0 = ex2(m - ref), w1 = ex2(m1 - ref);
+      m = top;
+      l = l * w0 + l1 * w1;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-    const float mref = m == -INFINITY ? 0.f : m;
-    float acc[kPer] = {}, l = 0.f;
-#pragma unroll 8
-    for (int p = shared ? warp : 0; p < np; p += step) {
-      const float2 ml = a.part_ml[at(p)];
-      const float w = ex2(ml.x - mref);
-      float v[kPer];
-      if constexpr (kPer == 4) {
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + at(p) * D + lane * 4);
-      } else {
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + at(p) * D + lane * 2);
+      for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * w0 + v[x] * w1;
+    };
+    constexpr int kBatch = 4;                       // pieces read at once
+    for (int p0 = shared ? warp : 0; p0 < np; p0 += kBatch * step) {
+      float2 ml[kBatch];
+      float v[kBatch][kPer];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int p = p0 + u * step;
+        if (p < np) {
+          ml[u] = a.part_ml[at(p)];
+          if constexpr (kPer == 4) {
+            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(a.part_o + at(p) * D + lane * 4);
+          } else {
+            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(a.part_o + at(p) * D + lane * 2);
+          }
+        }
       }
-      l += w * ml.y;
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) acc[x] += w * v[x];
+      for (int u = 0; u < kBatch; ++u)
+        if (p0 + u * step < np) add(ml[u].x, ml[u].y, v[u]);
     }
     if (shared) {
 #pragma unroll
       for (int x = 0; x < kPer; ++x) s_o[warp][lane * kPer + x] = acc[x];
-      if (lane == 0) s_l[warp] = l;
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
       __syncthreads();
       if (warp == 0) {
-        for (int w = 1; w < kCombineWarps; ++w) {
-          l += s_l[w];
+        const int used = min(kCombineWarps, np);
+        for (int w = 1; w < used; ++w) {
+          float v[kPer];
 #pragma unroll
-          for (int x = 0; x < kPer; ++x) acc[x] += s_o[w][lane * kPer + x];
+          for (int x = 0; x < kPer; ++x) v[x] = s_o[w][lane * kPer + x];
+          add(s_ml[w].x, s_ml[w].y, v);
         }
       }
     }
