@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   volatile int* abort_flag = misc + 0;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 1);
   int* found = misc + 2;                   // the share's first request, its T and L
-  long long* found_at = reinterpret_cast<long long*>(misc + 8);   // the request's first block on the line
+  long long* found_at = reinterpret_cast<long long*>(misc + 8);   // the share's start in it, the cost of a key head
   long long* wsum = reinterpret_cast<long long*>(misc + 16);      // [kWarps]
   TreePiece* pieces = reinterpret_cast<TreePiece*>(base + C::oPieces);
 
@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   bool bad = false;
   const bool masked = a.mask != nullptr;
   TreeReq mine{0, 0, 0, 0};
-  long long cost = 0, upto = 0, total = 0;    // of the thread's request, of the requests up to it, of all
+  long long per_head = 0, cost = 0;           // of the thread's request
+  long long upto = 0, total = 0;              // of the requests up to it, of all
   auto scan = [&](long long v) {              // inclusive over the CTA; `total` grows by the sum
     const long long before = total;
     upto = v;
@@ -493,7 +494,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     cost = 0;
     if (r < a.R) {
       mine = tree_request(a, r, &bad);
-      cost = tree_cost_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
+      per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
+      cost = per_head * a.Hkv;
     }
     scan(cost);
   }
@@ -508,7 +510,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       found[0] = r;
       found[1] = mine.T;
       found[2] = mine.L;
-      *found_at = upto - cost;
+      found_at[0] = share0 - (upto - cost);
+      found_at[1] = per_head;
     }
   };
   if (a.R <= C::kThreads) {
@@ -521,7 +524,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       cost = 0;
       if (r < a.R) {
         mine = tree_request(a, r, &again);
-        cost = tree_cost_before(mine, mine.tiles, a.TT, masked) * a.Hkv;
+        per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
+        cost = per_head * a.Hkv;
       }
       scan(cost);
       find(r);
@@ -574,20 +578,23 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       w.q.nb = (w.q.L + w.q.T + kBlock - 1) / kBlock;
       w.q.tiles = (w.q.T + a.TT - 1) / a.TT;
       w.left = share1 - share0;
-      const long long per_head = tree_cost_before(w.q, w.q.tiles, a.TT, masked);
-      long long x = share0 - *found_at;
+      const long long per_head = found_at[1];
+      long long x = found_at[0], at_tile = 0;
       w.head = static_cast<int>(div64(x, per_head));
       x -= w.head * per_head;
       int lo = 0, hi = w.q.tiles;             // the last tile that begins at or before x
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tree_cost_before(w.q, mid, a.TT, masked) <= x)
+        const long long v = tree_cost_before(w.q, mid, a.TT, masked);
+        if (v <= x) {
           lo = mid;
-        else
+          at_tile = v;
+        } else {
           hi = mid;
+        }
       }
       w.tile = lo;
-      ld.more = w.begin(a, static_cast<int>(x - tree_cost_before(w.q, lo, a.TT, masked)));
+      ld.more = w.begin(a, static_cast<int>(x - at_tile));
     }
     if (ld.more) {
       ld.open(a, lane);
