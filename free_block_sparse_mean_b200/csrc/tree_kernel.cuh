@@ -375,29 +375,22 @@ struct TreePiece {
   int pad;
 };
 
-// A walk block by block, for the loads. The lanes hold the ids of the 32 pages from `base`
-// on, and of the 32 behind them, read a window ahead of their use: a read of one id a
-// block cost its warp 700 cycles a block. (A block's pages never lie in two windows.)
-struct TreeLoad {
-  TreeWalk w;
-  int k;                          // block of the piece
-  bool more;
+// The page ids of a request, for the loads: the lanes hold those of the 32 pages from
+// `base` on, and of the 32 behind them, read a window ahead of their use (a read of one id a
+// block cost its warp 700 cycles a block). A block's pages never lie in two windows.
+struct TreePages {
   const int* row;
   int base, pages, ids, ahead;
   __device__ __forceinline__ int read(int p) const { return p < pages ? row[p] : 0; }
-  __device__ __forceinline__ void open(const TreeArgs& a, int lane) {
-    k = 0;
-    row = a.table + static_cast<long long>(w.r) * a.width;
-    pages = (w.q.L + w.q.T + (1 << a.page_shift) - 1) >> a.page_shift;
-    base = (w.b0 * kBlock) >> a.page_shift;
+  __device__ __forceinline__ void open(const TreeArgs& a, int r, int keys, int b0, int lane) {
+    row = a.table + static_cast<long long>(r) * a.width;
+    pages = (keys + (1 << a.page_shift) - 1) >> a.page_shift;
+    base = (b0 * kBlock) >> a.page_shift;
     ids = read(base + lane);
     ahead = read(base + 32 + lane);
   }
-  __device__ __forceinline__ void step(const TreeArgs& a, int lane) {
-    if (++k == w.n) {
-      more = w.next(a);
-      if (more) open(a, lane);
-    } else if (((w.b0 + k) * kBlock >> a.page_shift) >= base + 32) {
+  __device__ __forceinline__ void advance(const TreeArgs& a, int block, int lane) {
+    if ((block * kBlock >> a.page_shift) >= base + 32) {
       base += 32;
       ids = ahead;
       ahead = read(base + 32 + lane);
@@ -454,7 +447,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     uint64_t* bar = bars + threadIdx.x;
     int count = 1;
     if ((bar >= kempty && bar < vfull) || (bar >= vempty && bar < vready)) count = NC;
-    if (bar >= piece_empty && bar < q_full) count = 1 + 6 * NC;
+    if (bar >= piece_empty && bar < q_full) count = NC + 6 * NC;      // V's loads of two chains read pieces too
     if (bar >= p_full && bar < pv_done) count = 4;
     if (bar >= pv_done && bar < drain) count = 2;
     if (bar == drain) count = 2 * NC;
@@ -560,114 +553,145 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   // the chain has rows in the piece
   auto active = [&](const TreePiece* p, int c) { return p->tile * a.TT + c * a.TC < p->T; };
 
+  // One block of K or V into a stage of its ring: each lane's page and box of it.
+  bool bad_page = false;
+  auto load_block = [&](const TreePages& pg, uint8_t* dst, const CUtensorMap* map, uint64_t* full, int block, int keys,
+                        int head) {
+    const int at = block * kBlock + sub_off;
+    const int boxes = (min(keys - block * kBlock, kBlock) + sub - 1) >> sub_shift;
+    int id = __shfl_sync(FULL, pg.ids, (at >> a.page_shift) - pg.base);
+    if (lane == 0) mbar_expect_tx(full, static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks);
+    __syncwarp();
+    if (loads && at < keys) {
+      if (id < 0 || id >= a.pages) {
+        bad_page = true;
+        id = 0;                                   // flagged; any page of the pool keeps the load in bounds
+      }
+      tma_load_5d(dst + dst_off, map, 0, at & (page - 1), my_chunk, head, id, full);
+    }
+  };
+  // every load that was issued has landed before the CTA leaves (bounded)
+  auto drain_loads = [&](uint64_t* full, int issued) {
+    if (lane == 0) {
+      for (int b = max(0, issued - C::ST); b < issued; ++b)
+        mbar_wait_drain(&full[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
+    }
+  };
+  // what a wait for the stage's previous block waits for
+  auto before = [](int n) { return static_cast<uint32_t>(n / C::ST - 1) & 1u; };
+
   if (warp == 0) {
-    // ------------------------------------------------------------ pieces, K and V loads
+    // ------------------------------------------------------------ pieces, K loads (one chain: V loads too)
     // stage k % ST holds block k of the share, loaded when the products that read block
     // k - ST have completed
     if (lane == 0) {
       tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+      if (NC == 1) tma_prefetch_desc(&tmV);
     }
-    bool bad_page = false;
-    TreeLoad ld;
-    {
-      TreeWalk& w = ld.w;
-      w.r = found[0];
-      w.q.T = found[1];
-      w.q.L = found[2];
-      w.q.nb = (w.q.L + w.q.T + kBlock - 1) / kBlock;
-      w.q.tiles = (w.q.T + a.TT - 1) / a.TT;
-      w.left = share1 - share0;
-      const long long per_head = found_at[1];
-      long long x = found_at[0], at_tile = 0;
-      w.head = static_cast<int>(div64(x, per_head));
-      x -= w.head * per_head;
-      int lo = 0, hi = w.q.tiles;             // the last tile that begins at or before x
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        const long long v = tree_cost_before(w.q, mid, a.TT, masked);
-        if (v <= x) {
-          lo = mid;
-          at_tile = v;
-        } else {
-          hi = mid;
-        }
+    TreeWalk w;
+    w.r = found[0];
+    w.q.T = found[1];
+    w.q.L = found[2];
+    w.q.nb = (w.q.L + w.q.T + kBlock - 1) / kBlock;
+    w.q.tiles = (w.q.T + a.TT - 1) / a.TT;
+    w.left = share1 - share0;
+    const long long head_cost = found_at[1];
+    long long x = found_at[0], at_tile = 0;
+    w.head = static_cast<int>(div64(x, head_cost));
+    x -= w.head * head_cost;
+    int lo = 0, hi = w.q.tiles;                   // the last tile that begins at or before x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      const long long v = tree_cost_before(w.q, mid, a.TT, masked);
+      if (v <= x) {
+        lo = mid;
+        at_tile = v;
+      } else {
+        hi = mid;
       }
-      w.tile = lo;
-      ld.more = w.begin(a, static_cast<int>(x - at_tile));
     }
-    if (ld.more) {
-      ld.open(a, lane);
-    } else if (lane == 0) {                   // no block at all: an empty piece for the others
+    w.tile = lo;
+    bool more = w.begin(a, static_cast<int>(x - at_tile));
+    if (!more && lane == 0) {                     // no block at all: an empty piece for the others
       pieces[0] = TreePiece{};
       pieces[0].last = 1;
       mbar_arrive(&piece_full[0]);
     }
-    int nk = 0, nv = 0, item = 0, nw = 0;     // loads issued, pieces written, blocks seen in part
-    while (ld.more) {
-      const int s = nk % C::ST;
-      const uint32_t before = static_cast<uint32_t>(nk / C::ST - 1) & 1u;
-      const int at = (ld.w.b0 + ld.k) * kBlock + sub_off, keys = ld.w.q.L + ld.w.q.T;   // the lane's box
-      const int boxes = (min(keys - at + sub_off, kBlock) + sub - 1) >> sub_shift;
-      const uint32_t bytes = static_cast<uint32_t>(boxes) * sub * 128 * C::kChunks;
-      int id = __shfl_sync(FULL, ld.ids, (at >> a.page_shift) - ld.base);
-      const bool mine_loads = loads && at < keys;
-      if (mine_loads && (id < 0 || id >= a.pages)) {
-        bad_page = true;
-        id = 0;                                   // flagged; any page of the pool keeps the load in bounds
-      }
-      if (nk >= C::ST && !warp_wait(&kempty[s], before, abort_flag)) break;
-      if (ld.k == 0 && item >= C::kPieces &&
+    int k = 0, nk = 0, nw = 0;                    // blocks of the share, K loads, blocks seen in part
+    for (int item = 0; more; ++item) {
+      if (item >= C::kPieces &&
           !warp_wait(&piece_empty[item % C::kPieces], static_cast<uint32_t>(item / C::kPieces - 1) & 1u, abort_flag))
         break;
+      const int keys = w.q.L + w.q.T;
+      TreePages pg;
+      pg.open(a, w.r, keys, w.b0, lane);
       if (lane == 0) {
-        mbar_expect_tx(&kfull[s], bytes);
-        if (ld.k == 0) {
-          TreePiece* p = &pieces[item % C::kPieces];
-          p->r = ld.w.r;
-          p->tok0 = a.starts[ld.w.r];
-          p->L = ld.w.q.L;
-          p->T = ld.w.q.T;
-          p->head = ld.w.head;
-          p->tile = ld.w.tile;
-          p->b0 = ld.w.b0;
-          p->n = ld.w.n;
-          p->nbt = ld.w.nbt;
-          p->last = ld.w.last();
-          p->special = 0;
-          if (ld.w.b0 == 0 && ld.w.n < ld.w.nbt)       // (its blocks are the share's last)
-            a.cut[cta] = make_int4(p->tok0 + p->tile * a.TT, min(a.TT, p->T - p->tile * a.TT) * a.G, p->head,
-                                   tree_owner(all, share1 - p->n + p->nbt - 1, ctas));
-          mbar_arrive(&piece_full[item % C::kPieces]);
+        TreePiece* p = &pieces[item % C::kPieces];
+        p->r = w.r;
+        p->tok0 = a.starts[w.r];
+        p->L = w.q.L;
+        p->T = w.q.T;
+        p->head = w.head;
+        p->tile = w.tile;
+        p->b0 = w.b0;
+        p->n = w.n;
+        p->nbt = w.nbt;
+        p->last = w.last();
+        p->special = 0;
+        if (w.b0 == 0 && w.n < w.nbt)             // (its blocks are the share's last)
+          a.cut[cta] = make_int4(p->tok0 + p->tile * a.TT, min(a.TT, p->T - p->tile * a.TT) * a.G, p->head,
+                                 tree_owner(all, share1 - p->n + p->nbt - 1, ctas));
+        mbar_arrive(&piece_full[item % C::kPieces]);
+      }
+      __syncwarp();
+      const int part = first_part(masked ? w.q.L : w.q.L + w.tile * a.TT + 1, w.b0);
+      int i = 0;
+      for (; i < w.n; ++i, ++k) {
+        const int s = k % C::ST;
+        pg.advance(a, w.b0 + i, lane);
+        if (k >= C::ST && !warp_wait(&kempty[s], before(k), abort_flag)) break;
+        load_block(pg, sK + s * C::kKVBytes, &tmK, &kfull[s], w.b0 + i, keys, w.head);
+        nk = k + 1;
+        if (NC == 1) {
+          if (k >= C::ST && !warp_wait(&vempty[s], before(k), abort_flag)) break;
+          load_block(pg, sV + s * C::kKVBytes, &tmV, &vfull[s], w.b0 + i, keys, w.head);
+          if (i >= part) {
+            if (lane == 0) mbar_arrive(&vpart[nw % C::ST]);
+            ++nw;
+          }
         }
       }
-      __syncwarp();
-      if (mine_loads)
-        tma_load_5d(sK + s * C::kKVBytes + dst_off, &tmK, 0, at & (page - 1), my_chunk, ld.w.head, id, &kfull[s]);
-      ++nk;
-      if (ld.k == 0) ++item;
-      if (nk > C::ST && !warp_wait(&vempty[s], before, abort_flag)) break;
-      const bool part =
-          ld.k >= first_part(masked ? ld.w.q.L : ld.w.q.L + ld.w.tile * a.TT + 1, ld.w.b0);
-      if (lane == 0) {
-        mbar_expect_tx(&vfull[s], bytes);
-        if (part) mbar_arrive(&vpart[nw % C::ST]);
+      if (i < w.n) break;
+      more = w.next(a);
+    }
+    drain_loads(kfull, nk);
+    if (NC == 1) drain_loads(vfull, k);
+  } else if (NC == 2 && warp == 2 + 2 * NC) {
+    // ------------------------------------------------------------ V loads
+    if (lane == 0) tma_prefetch_desc(&tmV);
+    int k = 0, nw = 0;
+    for (int item = 0;; ++item) {
+      const TreePiece* p = piece(item);
+      if (!p) break;
+      const int keys = p->L + p->T, n = p->n, b0 = p->b0, head = p->head, last = p->last;
+      const int part = first_part(masked ? p->L : p->L + p->tile * a.TT + 1, b0);
+      TreePages pg;
+      pg.open(a, p->r, keys, b0, lane);
+      release(item);
+      int i = 0;
+      for (; i < n; ++i, ++k) {
+        const int s = k % C::ST;
+        pg.advance(a, b0 + i, lane);
+        if (k >= C::ST && !warp_wait(&vempty[s], before(k), abort_flag)) break;
+        load_block(pg, sV + s * C::kKVBytes, &tmV, &vfull[s], b0 + i, keys, head);
+        if (i >= part) {
+          if (lane == 0) mbar_arrive(&vpart[nw % C::ST]);
+          ++nw;
+        }
       }
-      if (part) ++nw;
-      __syncwarp();
-      if (mine_loads)
-        tma_load_5d(sV + s * C::kKVBytes + dst_off, &tmV, 0, at & (page - 1), my_chunk, ld.w.head, id, &vfull[s]);
-      ++nv;
-      ld.step(a, lane);
+      if (i < n || last) break;
     }
-    if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
-    // every load that was issued has landed before the CTA leaves (bounded)
-    if (lane == 0) {
-      for (int b = max(0, nk - C::ST); b < nk; ++b)
-        mbar_wait_drain(&kfull[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
-      for (int b = max(0, nv - C::ST); b < nv; ++b)
-        mbar_wait_drain(&vfull[b % C::ST], static_cast<uint32_t>(b / C::ST) & 1u);
-    }
+    drain_loads(vfull, k);
   } else if (warp == 1) {
     // ------------------------------------------------------------ Q loads, what a V block holds unseen
     if (lane == 0) tma_prefetch_desc(&tmQ);
@@ -1051,6 +1075,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       if (last) break;
     }
   }
+  if (bad_page) atomicOr(&g_dev_error, DEVERR_RANGE);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
