@@ -260,9 +260,7 @@ sa_status sparse_attn_cache_write(const void* K, const void* V, int64_t token_st
   a.dst_head = c.Hkv > 1 ? c.head_stride / 8 : 0;
   a.rows = static_cast<unsigned>(rows);
   a.H = static_cast<unsigned>(c.Hkv);
-  a.n = static_cast<unsigned>(n);
   a.page_shift = log2_exact(c.page_size);
-  a.head_first = 0;
   a.slot_end = static_cast<long long>(c.pages) * c.page_size;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int per = (256 / (c.d / 8)) * 4;             // rows of a CTA
