@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
 // block once for 256 rows; a tile of at most 128 rows has one chain, two CTAs on an SM.
 // kSmallQ: the tile has at most 32 rows, so Q takes 32 rows of shared memory (twice, so
 // that the next tile's is there early) and the freed space a third stage of K and of V.
-// The S product still reads 128 rows (rows behind Q are whatever lies there); a row's
+// The S product reads 64 rows (those behind Q are whatever lies there); a row's
 // result touches no other row, and the rows that do not exist are never written out.
 template <int D, int NC, bool kSmallQ>
 struct TreeCfg {
@@ -84,6 +84,8 @@ struct TreeCfg {
   static constexpr int kThreads = 256 * NC;                // 4 NC warps that issue, 4 NC softmax warps
   static constexpr int kCtas = NC == 1 ? 2 : 1;            // on an SM
   static constexpr int kChunks = D / 64;
+  static constexpr int kM = kSmallQ ? 64 : 128;            // rows of the products
+  static constexpr int kWarpRows = kM / 4;                 // in each TMEM lane quadrant, in its first lanes
   static constexpr int kQRows = kSmallQ ? 32 : 128;
   static constexpr int kQBufs = kSmallQ ? 2 : 1;
   static constexpr int kQChunkBytes = kQRows * 128;
@@ -404,8 +406,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a,
                     const uint16_t* __restrict__ Vraw, long long v_page, long long v_token, long long v_head) {
   using C = TreeCfg<D, NC, kSmallQ>;
-  constexpr uint32_t kIdescS = idesc_16_f32(kElem, 128, 64, false);
-  constexpr uint32_t kIdescPV = idesc_16_f32(kElem, 128, D, true);
+  constexpr uint32_t kIdescS = idesc_16_f32(kElem, C::kM, 64, false);
+  constexpr uint32_t kIdescPV = idesc_16_f32(kElem, C::kM, D, true);
   constexpr int kWarps = C::kThreads / 32;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* base = tree_smem;
@@ -888,7 +890,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     s_full += 2 * c;
     p_full += 2 * c;
     pv_done += 2 * c;
-    const int row = wq * 32 + lane;
+    const int row = wq * C::kWarpRows + lane;
     bool alive = true;
     int k = 0;                                     // blocks of the chain
     for (int item = 0; alive; ++item) {
@@ -897,7 +899,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       const int n = p->n, last = p->last;
       const int t0 = p->tile * a.TT + c * a.TC;
       const int rows = min(a.TC, p->T - t0) * a.G;            // rows of the chain that exist
-      if (wq * 32 >= rows) {
+      if (wq * C::kWarpRows >= rows) {
         for (int i = 0; rows > 0 && i < n; ++i, ++k) {
           if (!warp_wait(&s_full[k & 1], static_cast<uint32_t>(k >> 1) & 1u, abort_flag)) {
             alive = false;
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         if (last) break;
         continue;
       }
-      const bool valid = row < rows;
+      const bool valid = row < rows && lane < C::kWarpRows;
       const int b0 = p->b0;
       const int open = masked ? p->L : p->L + t0 + 1;         // every row of the chain sees the keys before it
       float m_ref = -INFINITY, l = 0.f;
