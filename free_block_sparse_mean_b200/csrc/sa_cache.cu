@@ -321,6 +321,7 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   a.O = O;
   a.o_token = s.n > 1 ? o_token : 0;
   a.o_head = Hq > 1 ? o_head : 0;
+  a.o_wide = aligned(O, 32) && a.o_token % 16 == 0 && a.o_head % 16 == 0;
   a.lse = lse;
   a.scale_log2 = scale * 1.4426950408889634f;
   if (L.split) {

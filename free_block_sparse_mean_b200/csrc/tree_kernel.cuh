@@ -115,6 +115,7 @@ struct TreeArgs {
   int min_cost;                   // smallest share of a CTA
   void* O;
   long long o_token, o_head;      // strides in elements
+  int o_wide;                     // rows of O are 32-byte aligned
   float* lse;                     // [n][Hkv * G] or null
   float scale_log2;
   float* part_o;                  // [2 * CTA + (0: the piece ends its tile, or 1: begins it)][TT * G][D]
@@ -124,7 +125,7 @@ struct TreeArgs {
 };
 
 struct TreeReq {
-  int T, L, nb, tiles;
+  int T, L, nb, tiles, tok0;      // new and cached tokens, key blocks, tiles, first row of the step
 };
 
 // Request r as the kernels take it: T = 0 if it has nothing to compute or its
@@ -134,6 +135,7 @@ __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int r, bool* 
   const int s0 = a.starts[r], s1 = a.starts[r + 1];
   q.L = a.lens[r];
   q.T = s1 - s0;
+  q.tok0 = s0;
   const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.n;
   if (a.granted) q.T = min(q.T, max(a.granted[r], 0));
   if (!ok || (q.T > 0 && (q.L < 0 || static_cast<long long>(q.L) + q.T >
@@ -213,6 +215,13 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
       : "memory");
+}
+
+// 32 bytes, a whole sector, to a 32-byte aligned address.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // True in one thread of the warp, the same one every time. The compiler keeps what is
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   int* misc = reinterpret_cast<int*>(base + C::oMisc);
   volatile int* abort_flag = misc + 0;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 1);
-  int* found = misc + 2;                   // the share's first request, its T and L
+  int* found = misc + 2;                   // the share's first request, its T, L and first row
   long long* found_at = reinterpret_cast<long long*>(misc + 8);   // the share's start in it, the cost of a key head
   long long* wsum = reinterpret_cast<long long*>(misc + 16);      // [kWarps]
   TreePiece* pieces = reinterpret_cast<TreePiece*>(base + C::oPieces);
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   const int cta = static_cast<int>(blockIdx.x);
   bool bad = false;
   const bool masked = a.mask != nullptr;
-  TreeReq mine{0, 0, 0, 0};
+  TreeReq mine{};
   long long per_head = 0, cost = 0;           // of the thread's request
   long long upto = 0, total = 0;              // of the requests up to it, of all
   auto scan = [&](long long v) {              // inclusive over the CTA; `total` grows by the sum
@@ -505,6 +514,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       found[0] = r;
       found[1] = mine.T;
       found[2] = mine.L;
+      found[3] = mine.tok0;
       found_at[0] = share0 - (upto - cost);
       found_at[1] = per_head;
     }
@@ -594,6 +604,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     w.r = found[0];
     w.q.T = found[1];
     w.q.L = found[2];
+    w.q.tok0 = found[3];
     w.q.nb = (w.q.L + w.q.T + kBlock - 1) / kBlock;
     w.q.tiles = (w.q.T + a.TT - 1) / a.TT;
     w.left = share1 - share0;
@@ -630,7 +641,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       if (lane == 0) {
         TreePiece* p = &pieces[item % C::kPieces];
         p->r = w.r;
-        p->tok0 = a.starts[w.r];
+        p->tok0 = w.q.tok0;
         p->L = w.q.L;
         p->T = w.q.T;
         p->head = w.head;
@@ -1050,19 +1061,22 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
             }
           }
           if (whole_row) {
+            uint32_t w[16];
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
-              uint4 w;
-              w.x = pack16x2<kElem>(o[x + 0] * mul, o[x + 1] * mul);
-              w.y = pack16x2<kElem>(o[x + 2] * mul, o[x + 3] * mul);
-              w.z = pack16x2<kElem>(o[x + 4] * mul, o[x + 5] * mul);
-              w.w = pack16x2<kElem>(o[x + 6] * mul, o[x + 7] * mul);
-              *reinterpret_cast<uint4*>(orow + cc + x) = w;
+            for (int x = 0; x < 16; ++x) w[x] = pack16x2<kElem>(o[2 * x] * mul, o[2 * x + 1] * mul);
+            if (a.o_wide) {
+              st_global_32(orow + cc, w);
+              st_global_32(orow + cc + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(orow + cc + 8 * x) =
+                    make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
             }
           } else {
-            float4* to = reinterpret_cast<float4*>(a.part_o + prow * D + cc);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 32; x += 8)
+              st_global_32(a.part_o + prow * D + cc + x, reinterpret_cast<const uint32_t*>(o) + x);
           }
         }
       }
