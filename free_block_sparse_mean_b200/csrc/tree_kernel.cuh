@@ -1027,58 +1027,76 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       const long long token = static_cast<long long>(p->tok0) + t;
       const long long prow = (2LL * cta + (b0 == 0 ? 1 : 0)) * (a.TT * a.G) + c * a.TC * a.G + row;
       uint16_t* orow = static_cast<uint16_t*>(a.O) + token * a.o_token + hq * a.o_head;
-      tmem_ld32(o_addr, s0);
+      if (__builtin_expect(fix, 0)) {
+        // The elements taken out of V (from the tile's `open` on) are added to O, for the
+        // rows that see their token. Apart from the pass below: in it, this code cost every
+        // piece its instruction fetches (500 requests of up to 500 tokens: 152 us for 125).
+        const int out0 = masked ? p->L : p->L + p->tile * a.TT + 1;
+        const int* trow = a.table + static_cast<long long>(p->r) * a.width;
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          float o[32];
+          tmem_ld32(o_addr + cc, o);
+          tmem_wait_ld();
+          pin32(o);
+          for (int kb = b0 * kBlock; valid && kb < (b0 + n) * kBlock; kb += kBlock) {
+            if (kb + kBlock <= out0) continue;
+            unsigned long long vis = tree_visible(a, p->L, p->T, t, token, kb);
+            if (out0 > kb) vis &= ~low_bits64(out0 - kb);
+            for (; vis; vis &= vis - 1) {
+              const int at = kb + __ffsll(static_cast<long long>(vis)) - 1;
+              const int id = trow[at >> a.page_shift];
+              if (id < 0 || id >= a.pages) continue;
+              const uint16_t* v = Vraw + id * v_page + (at & (page - 1)) * v_token + p->head * v_head + cc;
 #pragma unroll
-      for (int cc = 0; cc < D; cc += 32) {
-        float(&o)[32] = (cc & 32) ? s1 : s0;
-        tmem_wait_ld();
-        pin32(o);
-        if (cc + 32 < D) tmem_ld32(o_addr + cc + 32, (cc & 32) ? s0 : s1);   // comes in under this one's stores
-        if (valid) {
-          if (l == 0.f) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0.f;
-          }
-          if (fix) {
-            // the elements taken out of V (from the tile's `open` on), for the rows that see their token
-            const int out0 = masked ? p->L : p->L + p->tile * a.TT + 1;
-            const int* trow = a.table + static_cast<long long>(p->r) * a.width;
-            for (int kb = b0 * kBlock; kb < (b0 + n) * kBlock; kb += kBlock) {
-              if (kb + kBlock <= out0) continue;
-              unsigned long long vis = tree_visible(a, p->L, p->T, t, token, kb);
-              if (out0 > kb) vis &= ~low_bits64(out0 - kb);
-              for (; vis; vis &= vis - 1) {
-                const int at = kb + __ffsll(static_cast<long long>(vis)) - 1;
-                const int id = trow[at >> a.page_shift];
-                if (id < 0 || id >= a.pages) continue;
-                const uint16_t* v = Vraw + id * v_page + (at & (page - 1)) * v_token + p->head * v_head + cc;
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                  const uint32_t e = v[x];
-                  if (not_finite16<kElem>(e)) o[x] += to_float16<kElem>(e);
-                }
+              for (int x = 0; x < 32; ++x) {
+                const uint32_t e = v[x];
+                if (not_finite16<kElem>(e)) o[x] += to_float16<kElem>(e);
               }
             }
           }
-          if (whole_row) {
-            uint32_t w[16];
+          __syncwarp();
+          tmem_st32(o_addr + cc, o);
+        }
+        tmem_wait_st();
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 64) {
+        tmem_ld32(o_addr + cc, s0);
+        tmem_ld32(o_addr + cc + 32, s1);
+        tmem_wait_ld();
+        pin32(s0);
+        pin32(s1);
+        if (valid) {
+          if (l == 0.f) {                             // nothing was seen: 0 whatever the products were
 #pragma unroll
-            for (int x = 0; x < 16; ++x) w[x] = pack16x2<kElem>(o[2 * x] * mul, o[2 * x + 1] * mul);
+            for (int x = 0; x < 32; ++x) s0[x] = s1[x] = 0.f;
+          }
+          if (whole_row) {
+            uint32_t w[32];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              w[x] = pack16x2<kElem>(s0[2 * x] * mul, s0[2 * x + 1] * mul);
+              w[x + 16] = pack16x2<kElem>(s1[2 * x] * mul, s1[2 * x + 1] * mul);
+            }
             if (a.o_wide) {
-              st_global_32(orow + cc, w);
-              st_global_32(orow + cc + 16, w + 8);
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) st_global_32(orow + cc + 2 * x, w + x);
             } else {
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(orow + cc + 8 * x) =
-                    make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+              for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<uint4*>(orow + cc + 2 * x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
             }
           } else {
+            float* to = a.part_o + prow * D + cc;
 #pragma unroll
-            for (int x = 0; x < 32; x += 8)
-              st_global_32(a.part_o + prow * D + cc + x, reinterpret_cast<const uint32_t*>(o) + x);
+            for (int x = 0; x < 32; x += 8) {
+              st_global_32(to + x, reinterpret_cast<const uint32_t*>(s0) + x);
+              st_global_32(to + 32 + x, reinterpret_cast<const uint32_t*>(s1) + x);
+            }
           }
         }
+        __syncwarp();
       }
       if (valid) {
         if (!whole_row)
