@@ -217,6 +217,19 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// True if the phase with the given parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // 32 bytes, a whole sector, to a 32-byte aligned address.
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -978,8 +991,17 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         uint32_t pk[16];
         tree_exp32<kElem>(s0, a.scale_log2, -mref, acc0, acc1, pk);
         tmem_st16u(s_addr + (k & 1) * 64, pk);
+        // S(k+1), if it is there already, comes in under the second half
+        const uint32_t s_next = s_addr + ((k + 1) & 1) * 64;
+        const bool early = NC == 2 && i + 1 < n &&
+                           __all_sync(FULL, mbar_test(&s_full[(k + 1) & 1], static_cast<uint32_t>((k + 1) >> 1) & 1u));
+        if (early) {
+          tc_fence_after();
+          tmem_ld32(s_next, s0);
+        }
         tree_exp32<kElem>(s1, a.scale_log2, -mref, acc0, acc1, pk);
         tmem_st16u(s_addr + (k & 1) * 64 + 16, pk);
+        if (early) tmem_ld32(s_next + 32, s1);
         float r0, r1, r2, r3;
         f2unpack(acc0, r0, r1);
         f2unpack(acc1, r2, r3);
@@ -1005,14 +1027,14 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[k & 1]);
-        if (i + 1 < n) {
+        if (i + 1 < n && !early) {
           if (!warp_wait(&s_full[(k + 1) & 1], static_cast<uint32_t>((k + 1) >> 1) & 1u, abort_flag)) {
             alive = false;
             break;
           }
           tc_fence_after();
-          tmem_ld32(s_addr + ((k + 1) & 1) * 64, s0);
-          tmem_ld32(s_addr + ((k + 1) & 1) * 64 + 32, s1);
+          tmem_ld32(s_next, s0);
+          tmem_ld32(s_next + 32, s1);
         }
       }
       tmem_wait_ld();
