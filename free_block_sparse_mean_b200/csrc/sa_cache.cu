@@ -18,6 +18,7 @@
 namespace {
 
 constexpr int kSMs = 148;                       // B200
+constexpr int64_t kMaxPlaces = 0x7fffffff - 1024;   // places of a request: the sums of one and a block stay ints
 constexpr int kTreeMinCost = 3;                 // smallest share of a CTA, in 64-key blocks
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -52,7 +53,7 @@ sa_status check_step(const sa_step& s, int page_size) {
     return SA_ERR_INVALID_ARG;
   if (s.R > sa::kCacheMaxRequests) return SA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(s.R) * s.width > 0x7fffffff ||
-      static_cast<int64_t>(s.width) * page_size > 0x7fffffff)
+      static_cast<int64_t>(s.width) * page_size > kMaxPlaces)
     return SA_ERR_UNSUPPORTED;
   if (s.mask ? (s.words < 1 || s.words > 32) : s.words != 0) return SA_ERR_INVALID_ARG;
   return SA_OK;
@@ -203,7 +204,7 @@ sa_status sparse_attn_cache_plan(const int32_t* lens, const int32_t* new_tokens,
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
     return SA_ERR_UNSUPPORTED;
   if (R > sa::kCacheMaxRequests || static_cast<int64_t>(pages) * page_size > 0x7fffffff ||
-      static_cast<int64_t>(R) * width > 0x7fffffff || static_cast<int64_t>(width) * page_size > 0x7fffffff)
+      static_cast<int64_t>(R) * width > 0x7fffffff || static_cast<int64_t>(width) * page_size > kMaxPlaces)
     return SA_ERR_UNSUPPORTED;
   const int bytes = (4 * R + 3) * static_cast<int>(sizeof(int));
   if (sa::set_smem(sa::cache_plan_kernel, (4 * sa::kCacheMaxRequests + 3) * static_cast<int>(sizeof(int))) != SA_OK)

@@ -6,44 +6,60 @@
 // over the L cached tokens of the request and the new tokens j that t sees (its row
 // of mask bits, or all up to itself), in one pass with a running maximum and sum.
 //
-// Rows. The G query heads that share a key head read the same keys, so a tile is up
-// to 128 rows of (new token, head of the group), token-major: TT = 128 / G tokens.
-// One TMA box {64, G heads, TT tokens} per 128-byte column chunk brings them.
+// Rows. The G query heads that share a key head read the same keys, so a chain of
+// products is up to 128 rows of (new token, head of the group), token-major: TC = 128 / G
+// tokens. One TMA box {64, G heads, TC tokens} per 128-byte column chunk brings them. A
+// request with more rows than that has tiles of two chains (256 rows) on one ring of
+// keys and values, so that each block is read once for both: one CTA on an SM, else two.
 //
-// Work. The lengths are on the GPU and ragged, so the calls' work is one line of key
+// Work. The lengths are on the GPU and ragged, so a call's work is one line of key
 // blocks: request by request, key head by key head, tile by tile, each tile's blocks in
-// order. `ctas` CTAs (two on every SM, fewer when that leaves less than min_blocks to
-// each) take equal shares of the line, whatever tiles they run through: every CTA
-// finds its share itself, from a scan over the requests. A tile that one CTA runs from
-// end to end is written to O; of a tile cut by the border between shares each CTA
-// leaves (max, sum, unnormalised O) in fp32 for tree_combine_kernel. A CTA cuts at
-// most two tiles, one at each end of its share, so 2 * ctas such pieces are all there
-// can be. Measured against one CTA for each tile or for a fixed number of blocks: see
-// the table of target sizes in the design notes of this kernel's launch.
+// order and a fixed cost behind them. `ctas` CTAs take equal shares of the line, whatever
+// tiles they run through: every CTA finds its share itself, from a scan over the requests.
+// A tile that one CTA runs from end to end is written to O; of a tile cut by the border
+// between shares each CTA leaves (max, sum, unnormalised O) in fp32 for
+// tree_combine_kernel. A CTA cuts at most two tiles, one at each end of its share, so
+// 2 * ctas such pieces are all there can be. (One CTA for each tile or for a fixed number
+// of blocks, the first form: 425 us for 64 ragged requests, 385 with four times as many
+// and smaller pieces, which then cost the short calls; the line: 363.)
 //
-// Keys. Per 64-key block a warp reads the block's page ids and issues one TMA box
-// (pages of 64 tokens and more) or one per page and column chunk (smaller pages). A page id is read only where the request has tokens; places behind the
-// last token in its page are masked in S by column, and their V rows are set to zero
-// in shared memory, since 0 * NaN is not 0. For the same reason V elements that are
-// not finite are taken out of blocks that some row does not see whole; the rows that
-// do see such a token get the element added at the end (see `special` below).
+// Keys. Per 64-key block a warp issues one TMA box (pages of 64 tokens and more) or one
+// per page and column chunk (smaller pages). A page id is read only where the request has
+// tokens; places behind the last token in its page are masked in S by column, and their V
+// rows are set to zero in shared memory, since 0 * NaN is not 0. For the same reason V
+// elements that are not finite are taken out of blocks that some row does not see whole;
+// the rows that do see such a token get the element added at the end (`special`).
 //
-// Roles (192 threads): warp 0 loads V and issues O += P V, warp 1 owns TMEM, loads Q and
-// K and issues S = Q K^T, warps 2..5 run the softmax (thread = row), the O correction
-// and the epilogue; a softmax warp whose 32 rows do not exist only keeps the barriers'
-// counts, so a single-token call pays the exponentials of one warp. TMEM (256 columns):
-// S(k) in [0,64) or [64,128) by k's parity, P(k) over its first half, O [128, 128 + D).
-// Two CTAs fit on an SM.
+// Roles. Of 4 NC warps that issue, 0 walks the share, writes a descriptor of each piece
+// for the others and loads K (and V, with one chain), 1 loads Q and deals with unseen V
+// rows, then one a chain issues S = Q K^T and one O += P V; with two chains one more
+// loads V. 4 NC warps run the softmax (thread = row), the O correction and the epilogue; one
+// whose rows do not exist only keeps the barriers' counts. TMEM, 256 columns a chain: S(k)
+// in [0,64) or [64,128) by k's parity, P(k) over its first half, O [128, 128 + D).
+// What a warp that issues does beside its products, its chain waits for: with the loads in
+// the warps of the products, a read of a page id a block, a wait for every V block or
+// descriptors of the MMAs built a thread, the 64-key block of two chains took 2,374 cycles;
+// now 1,750 (D = 128; 1,024 are the exponential unit's, 1,264 the tensor cores').
 //
-// Blocks are counted through the CTA's whole share, tiles included, and so are the
+// Blocks are counted through the CTA's whole share, pieces included, and so are the
 // barrier phases: block k uses ring stage k % ST. S(k+2) is issued once P(k).V has
 // finished, which needs P(k) of every softmax warp, so each has read S(k) and waited for
-// it; the softmax of k+1 runs meanwhile on an S that was there when it began. P(k) goes
+// it; the softmax of k+1 runs meanwhile on an S that is there when it begins. P(k) goes
 // over S(k): a warp stores its own rows after it has loaded them. A stage is refilled
-// after the product that read it has completed. A tile's first P.V overwrites O: its P
-// is published only after the softmax warps have read the tile before out of TMEM. The
+// after the products that read it have completed. A piece's first P.V overwrites O: its P
+// is published only after the softmax warps have read the piece before out of TMEM. The
 // softmax waits for P(k-1).V only to correct O. So no wait is ever more than one phase
 // behind its barrier.
+//
+// Measured (one B200, bf16 unless said, in a captured graph): 64 requests of 1..16,384
+// cached tokens, 32 / 8 heads of 128, one token each, fp16: 334 us, 2.2 GB, the copy rate;
+// one request of 4,096, 24 heads: 16 us for 50 MB, bound by its chain of set-up, load,
+// softmax, join; 16 requests x 64 drafted tokens: 188 us, 586 MB and 145 GFLOP; two chunks of
+// 2,048 tokens behind 30,000 and 7,080: 1,246 us, 1,054 TFLOP/s, bound by the chain of a
+// block's softmax and products at the power limit's clock. Tried and slower or no different:
+// chains taking turns at the exponentials (1,404 us), a part of them as polynomials on
+// the FMA pipe (1,406 to 1,469 for one in eight to one in two), exponentials ahead of the
+// block's maximum (1,441), registers split by setmaxnreg (spills).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -478,77 +494,61 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     mbar_init(bar, count);
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    found[0] = -1;
+  }
   // what is before in the stream has finished; what is behind may set itself up
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int cta = static_cast<int>(blockIdx.x);
   bool bad = false;
   const bool masked = a.mask != nullptr;
+  // a thread takes `per` requests in a row; one scan over the CTA places them on the line
   TreeReq mine{};
-  long long per_head = 0, cost = 0;           // of the thread's request
-  long long upto = 0, total = 0;              // of the requests up to it, of all
-  auto scan = [&](long long v) {              // inclusive over the CTA; `total` grows by the sum
-    const long long before = total;
-    upto = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(FULL, upto, o);
-      if (lane >= o) upto += x;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = upto;
-    __syncthreads();
-    upto += before;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) upto += wsum[w];
-      total += wsum[w];
-    }
-  };
-  for (int r0 = 0; r0 < a.R; r0 += C::kThreads) {
-    const int r = r0 + threadIdx.x;
-    cost = 0;
-    if (r < a.R) {
-      mine = tree_request(a, r, &bad);
-      per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
-      cost = per_head * a.Hkv;
-    }
-    scan(cost);
+  long long per_head = 0, cost = 0;           // of the thread's last request's key heads, of its requests
+  const int per = (a.R + C::kThreads - 1) / C::kThreads, r0 = static_cast<int>(threadIdx.x) * per;
+  for (int r = r0; r < min(r0 + per, a.R); ++r) {
+    mine = tree_request(a, r, &bad);
+    per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
+    cost += per_head * a.Hkv;
   }
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), div64(total + a.min_cost - 1, a.min_cost)));
+  long long upto = cost, all = 0;             // of the requests up to the thread's last, of all
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(FULL, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) wsum[warp] = upto;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += wsum[w];
+    all += wsum[w];
+  }
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), div64(all + a.min_cost - 1, a.min_cost)));
   if (threadIdx.x == 0 && a.cut) a.cut[cta] = make_int4(0, 0, 0, 0);
   if (cta == 0 && bad) atomicOr(&g_dev_error, DEVERR_VALUE);
   if (cta >= ctas) return;
-  const long long all = total, share0 = tree_share(all, cta, ctas), share1 = tree_share(all, cta + 1, ctas);
+  const long long share0 = tree_share(all, cta, ctas), share1 = tree_share(all, cta + 1, ctas);
   if (warp == 1) tmem_alloc(tmem_holder, NC * C::kChainCols);
-  auto find = [&](int r) {                    // the share's first place lies in the thread's request
-    if (cost > 0 && share0 >= upto - cost && share0 < upto) {
-      found[0] = r;
-      found[1] = mine.T;
-      found[2] = mine.L;
-      found[3] = mine.tok0;
-      found_at[0] = share0 - (upto - cost);
-      found_at[1] = per_head;
-    }
-  };
-  if (a.R <= C::kThreads) {
-    find(threadIdx.x);
-  } else {
-    total = 0;
-    for (int r0 = 0; r0 < a.R; r0 += C::kThreads) {
-      const int r = r0 + threadIdx.x;
-      bool again;
-      cost = 0;
-      if (r < a.R) {
-        mine = tree_request(a, r, &again);
+  if (share0 >= upto - cost && share0 < upto) {       // the share's first place lies in the thread's requests
+    int r = r0;
+    long long at = upto - cost;
+    if (per > 1) {
+      for (;; ++r) {
+        mine = tree_request(a, r, &bad);
         per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
-        cost = per_head * a.Hkv;
+        if (share0 < at + per_head * a.Hkv || r + 1 >= min(r0 + per, a.R)) break;
+        at += per_head * a.Hkv;
       }
-      scan(cost);
-      find(r);
-      if (share0 < total) break;
     }
+    found[0] = r;
+    found[1] = mine.T;
+    found[2] = mine.L;
+    found[3] = mine.tok0;
+    found_at[0] = share0 - at;
+    found_at[1] = per_head;
   }
   const int page = 1 << a.page_shift;
   // a block is 64 / sub boxes of `sub` tokens; below 64 tokens a box holds one
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     w.q.nb = (w.q.L + w.q.T + kBlock - 1) / kBlock;
     w.q.tiles = (w.q.T + a.TT - 1) / a.TT;
     w.left = share1 - share0;
-    const long long head_cost = found_at[1];
+    const long long head_cost = max(found_at[1], 1LL);
     long long x = found_at[0], at_tile = 0;
     w.head = static_cast<int>(div64(x, head_cost));
     x -= w.head * head_cost;
@@ -637,7 +637,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
       }
     }
     w.tile = lo;
-    bool more = w.begin(a, static_cast<int>(x - at_tile));
+    // (every share begins in some request while the lengths stay as they were)
+    bool more = found[0] >= 0 && w.begin(a, static_cast<int>(x - at_tile));
     if (!more && lane == 0) {                     // no block at all: an empty piece for the others
       pieces[0] = TreePiece{};
       pieces[0].last = 1;

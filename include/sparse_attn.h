@@ -404,7 +404,7 @@ typedef struct {
 typedef struct {
   int32_t R;               /* requests, 1..8192 */
   int32_t n;               /* rows of the step's token buffers */
-  int32_t width;           /* columns of table; R*width, width*page_size < 2^31 */
+  int32_t width;           /* columns of table; R*width, width*page_size <= 2^31 - 1025 */
   int32_t max_new;         /* the most new tokens of a request, or 0 if not known. It only
                               sizes the tiles: more tokens than this are still right */
   int32_t words;           /* words of a mask row, 1..32, or 0 with mask = NULL */
