@@ -289,7 +289,8 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   if (ss != SA_OK) return ss;
   if (Hq < 1 || Hq % c.Hkv != 0) return SA_ERR_INVALID_ARG;
   if (Hq / c.Hkv > 128) return SA_ERR_UNSUPPORTED;
-  if (!(std::isfinite(scale) && scale > 0.f)) return SA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(std::isfinite(scale_log2) && scale > 0.f)) return SA_ERR_INVALID_ARG;
   if ((s.n > 1 && (!good_stride(q_token) || !good_stride(o_token))) ||
       (Hq > 1 && (!good_stride(q_head) || !good_stride(o_head))))
     return SA_ERR_INVALID_ARG;
@@ -324,7 +325,7 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   a.o_head = Hq > 1 ? o_head : 0;
   a.o_wide = aligned(O, 32) && a.o_token % 16 == 0 && a.o_head % 16 == 0;
   a.lse = lse;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   if (L.split) {
     a.part_o = reinterpret_cast<float*>(ws + L.part_o);
     a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);

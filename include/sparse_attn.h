@@ -472,7 +472,7 @@ sa_status sparse_attn_cache_write(const void* K, const void* V, int64_t token_st
  *
  *   Q, O       [n][Hq][d] with their strides (elements, multiples of 8), Hq a multiple of
  *              c.Hkv, at most 128 query heads to a key head
- *   scale      finite, > 0
+ *   scale      > 0, below 2e38
  *   lse        [n][Hq] or NULL: natural log of the softmax sum, -inf where nothing is seen
  *   workspace  at least sparse_attn_tree_workspace_size bytes, 256-byte aligned; calls that
  *              may run at once need one each (so do two graphs replayed together)
