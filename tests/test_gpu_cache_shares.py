@@ -3,6 +3,7 @@ without rows in the second, many short pieces, more requests than threads, piece
 all sizes, outputs of other alignments, calls one after another on one stream."""
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -246,3 +247,65 @@ def test_offsets_behind_32_bits():
         assert torch.equal(x, y)
     moved = torch.cat([k[:50], k[50 + torch.tensor([1, 4, 5, 11])]])
     assert torch.equal(results[1][1], moved)
+
+
+def test_captured_behind_copies_and_joined_streams():
+    """A captured call whose inputs come from a copy on the same stream and from another stream
+    that joins right before it, and whose output another stream reads."""
+    kc, vc, table = cache_of([300, 9], [3, 3], 32, 2, 64, BF, 11, fill=0.0)
+    kc, vc = kc.cuda(), vc.cuda()
+    g = torch.Generator().manual_seed(5)
+    qs = [torch.randn(6, 4, 64, generator=g).to(BF).cuda() for _ in range(2)]
+    plan = sa.CachePlan(table=dev_ints(table), lens=dev_ints([300, 9]), starts=dev_ints([0, 3, 6]), max_new=3)
+    want = [sa.sparse_attn_tree_fwd(q, kc, vc, plan) for q in qs]
+    source, lens = torch.empty_like(qs[0]), dev_ints([300, 9])
+    q = torch.zeros_like(source)
+    plan.lens = torch.zeros_like(lens)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            plan.lens.copy_(lens)
+        q.copy_(source)
+        main.wait_stream(side)
+        o = sa.sparse_attn_tree_fwd(q, kc, vc, plan)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            twice = o + o
+        main.wait_stream(side)
+        q.fill_(math.nan)
+        plan.lens.fill_(-1)
+    for i in (0, 1, 0):
+        source.copy_(qs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[i]) and torch.equal(twice, want[i] + want[i])
+    no_device_error()
+
+
+def test_calls_from_two_threads():
+    """Threads with streams of their own; the first calls of a form may come from both at once."""
+    kc, vc, table = cache_of([600, 50], [5, 40], 16, 2, 128, HF, 12, fill=0.0)
+    kc, vc, table = kc.cuda(), vc.cuda(), dev_ints(table)
+    q = torch.randn(45, 4, 128, generator=torch.Generator().manual_seed(6)).to(HF).cuda()
+    plans = [sa.CachePlan(table=table, lens=dev_ints([600, 50]), starts=dev_ints([0, 5, 45]), max_new=m) for m in (5, 64)]
+    got = [[], []]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i].append(sa.sparse_attn_tree_fwd(q, kc, vc, plans[i]))
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        want = sa.sparse_attn_tree_fwd(q, kc, vc, plans[i])
+        assert len(got[i]) == 20 and all(torch.equal(o, want) for o in got[i])
+    no_device_error()
