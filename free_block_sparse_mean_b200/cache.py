@@ -63,44 +63,49 @@ class CachePlan:
     max_new: int = 0
 
 
+# The checks below are written for the host's time: a step of small requests costs its calls,
+# not its kernels (a plan of 64 requests 4 us of 18), and a check that passes is one
+# expression. What it refuses is looked at again for the message.
+_I32 = torch.int32
 _get_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _launch(name: str, dev, call, *args):
-    """The C call on the device's current torch stream. A step of small requests costs its
-    calls, not its kernels (4 us of 37 for a plan of 64 requests), so nothing here is
-    done that the case does not need: no device switch on the current device, no views."""
-    if _get_device() == dev.index:
-        st = call(*args, _raw_stream(dev.index))
+def _launch(name: str, index: int, call, *args):
+    """The C call on the GPU's current torch stream (no device switch if it is the current one)."""
+    if _get_device() == index:
+        st = call(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = call(*args, _raw_stream(dev.index))
+        with torch.cuda.device(index):
+            st = call(*args, _raw_stream(index))
     if st != _lib.SA_OK:
         raise SparseAttnError(name, st, _lib.load())
 
 
-def _ints(name: str, t: torch.Tensor, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or t.device != dev \
+def _ints(name: str, t: torch.Tensor, shape, index: int):
+    """t as a contiguous int32 tensor of the shape on the GPU; its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.shape != shape or t.get_device() != index \
             or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {dev}")
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on cuda:{index}")
+    return t.data_ptr()
 
 
-def _rows(name: str, t: torch.Tensor, dtype, dev):
-    if t.dim() != 3 or t.dtype is not dtype or t.device != dev:
+def _rows(name: str, t: torch.Tensor, dtype, index: int):
+    """t as rows [n, heads, d] of the type on the GPU; its address."""
+    if t.dim() != 3 or t.dtype is not dtype or t.get_device() != index:
         raise ValueError(f"{name} must be [n, heads, d] in the cache's type on its device")
-    _strides(name, t)
+    return _strides(name, t)
 
 
 def _strides(name: str, t: torch.Tensor):
-    """d contiguous, every other step a positive multiple of 8 elements, 16-byte base."""
-    good = t.data_ptr() % 16 == 0
-    if good and not (t.is_contiguous() and t.shape[-1] % 8 == 0):
+    """d contiguous, every other step a positive multiple of 8 elements, 16-byte base (the address returned)."""
+    ptr, shape = t.data_ptr(), t.shape
+    if ptr & 15 or not (t.is_contiguous() and shape[-1] & 7 == 0):
         st = t.stride()
-        good = st[-1] == 1 and all(s > 0 and s % 8 == 0 for s, e in zip(st[:-1], t.shape) if e > 1)
-    if not good:
-        raise ValueError(f"{name} must have a contiguous last dimension, strides that are positive multiples of 8 "
-                         "elements and a 16-byte aligned base")
+        if ptr & 15 or st[-1] != 1 or any(x <= 0 or x & 7 for x, e in zip(st[:-1], shape) if e > 1):
+            raise ValueError(f"{name} must have a contiguous last dimension, strides that are positive multiples of 8 "
+                             "elements and a 16-byte aligned base")
+    return ptr
 
 
 def _same_layout(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -108,41 +113,36 @@ def _same_layout(a: torch.Tensor, b: torch.Tensor) -> bool:
     return x == y or all(i == j for i, j, e in zip(x, y, a.shape) if e > 1)
 
 
-def _cache(k: torch.Tensor, v: torch.Tensor, dims: int = 4) -> SaCache:
-    dtype = _DTYPES.get(k.dtype)
-    if dtype is None or not k.is_cuda:
+def _cache(k: torch.Tensor, v: torch.Tensor, dims: int = 4):
+    """The caches' layout, their addresses and their GPU."""
+    dtype, index, shape = _DTYPES.get(k.dtype), k.get_device(), k.shape
+    if dtype is None or index < 0:
         raise ValueError("a cache must be a bf16 or fp16 CUDA tensor")
-    shape = k.shape
-    if len(shape) != dims or v.shape != shape or v.dtype is not k.dtype or v.device != k.device \
+    if len(shape) != dims or v.shape != shape or v.dtype is not k.dtype or v.get_device() != index \
             or not _same_layout(k, v):
         raise ValueError("the caches must be [pages, page_size, Hkv, d] of one type, shape and layout")
-    if k.numel() == 0:
+    if 0 in shape:
         raise ValueError("the caches must not be empty")
-    _strides("the cache", k)
-    _strides("the cache", v)
+    kp, vp = _strides("the cache", k), _strides("the cache", v)
     pages, page, heads, d = shape[-4:]
     ps, ts, hs, _ = k.stride()[-4:]
-    return SaCache(pages, page, heads, d, dtype, ps if pages > 1 else page * heads * d, ts, hs if heads > 1 else d)
+    return SaCache(pages, page, heads, d, dtype, ps if pages > 1 else page * heads * d, ts,
+                   hs if heads > 1 else d), kp, vp, index
 
 
-def _step(plan: CachePlan, n: int, dev, masked: bool = True) -> SaStep:
-    table, lens, starts, granted = plan.table, plan.lens, plan.starts, plan.granted
+def _step(plan: CachePlan, n: int, index: int, masked: bool = True) -> SaStep:
+    table, granted, mask, words = plan.table, plan.granted, None, 0
     if table.dim() != 2:
         raise ValueError("the plan's table must be [R, width]")
     R, width = shape = table.shape
-    _ints("the plan's table", table, shape, dev)
-    _ints("the plan's lens", lens, (R,), dev)
-    _ints("the plan's starts", starts, (R + 1,), dev)
     if granted is not None:
-        _ints("the plan's granted", granted, (R,), dev)
-        granted = granted.data_ptr()
-    words, mask = 0, None
+        granted = _ints("the plan's granted", granted, (R,), index)
     if masked and plan.mask is not None:
         words = plan.mask.shape[-1]
-        _ints("the plan's mask", plan.mask, (n, words), dev)
-        mask = plan.mask.data_ptr()
-    return SaStep(R, n, width, int(plan.max_new), words, starts.data_ptr(), lens.data_ptr(), granted, table.data_ptr(),
-                  mask)
+        mask = _ints("the plan's mask", plan.mask, (n, words), index)
+    return SaStep(R, n, width, int(plan.max_new), words, _ints("the plan's starts", plan.starts, (R + 1,), index),
+                  _ints("the plan's lens", plan.lens, (R,), index), granted,
+                  _ints("the plan's table", table, shape, index), mask)
 
 
 def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: torch.Tensor, held: torch.Tensor,
@@ -161,45 +161,44 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
     and nfree must not be this call's inputs); the returned plan's table, lens and
     free_pages are the ones given."""
     lib = _lib.load()
-    if not lens.is_cuda or table.dim() != 2:
+    index = lens.get_device()
+    if index < 0 or table.dim() != 2:
         raise ValueError("lens must be a CUDA tensor, table [R, width]")
-    dev = lens.device
     R, width = shape = table.shape
-    _ints("table", table, shape, dev)
-    for name, t in (("lens", lens), ("new_tokens", new_tokens), ("held", held)):
-        _ints(name, t, (R,), dev)
-    _ints("nfree", nfree, (1,), dev)
+    vec = (R,)
     if free_pages.dim() != 1:
         raise ValueError("free_pages must be [pages]")
-    _ints("free_pages", free_pages, free_pages.shape, dev)
     n, mask_words = int(n), int(mask_words)
     if n < 1 or mask_words < 0:
         raise ValueError("n must be at least 1 and mask_words at least 0")
+    ins = (_ints("lens", lens, vec, index), _ints("new_tokens", new_tokens, vec, index), _ints("held", held, vec, index),
+           _ints("nfree", nfree, (1,), index), _ints("free_pages", free_pages, free_pages.shape, index),
+           _ints("table", table, shape, index))
+    tree = None                                  # (the tensor itself stays referred to)
     if parents is not None:
         if mask_words == 0:
             raise ValueError("parents needs mask_words")
-        _ints("parents", parents, (n,), dev)
+        tree = _ints("parents", parents, (n,), index)
     if out is None:
         sizes = [R + 1, R, R, 1, n, n, n * mask_words]     # one buffer: an allocation costs more than a view
         starts, granted, held_out, nfree_out, slots, positions, mask = \
-            torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
+            lens.new_empty(sum(sizes)).split_with_sizes(sizes)
         out = CachePlan(table, lens, starts, granted, mask.view(n, mask_words) if mask_words else None, slots,
                         positions, held_out, nfree_out, free_pages, int(max_new))
     else:
-        for name, t, shape in (("starts", out.starts, (R + 1,)), ("granted", out.granted, (R,)),
-                               ("slots", out.slots, (n,)), ("positions", out.positions, (n,)),
-                               ("held", out.held, (R,)), ("nfree", out.nfree, (1,))):
-            _ints(f"out.{name}", t, shape, dev)
+        for name, t, want in (("starts", out.starts, (R + 1,)), ("granted", out.granted, vec), ("slots", out.slots, (n,)),
+                              ("positions", out.positions, (n,)), ("held", out.held, vec),
+                              ("nfree", out.nfree, (1,))):
+            _ints(f"out.{name}", t, want, index)
         if mask_words:
-            _ints("out.mask", out.mask, (n, mask_words), dev)
+            _ints("out.mask", out.mask, (n, mask_words), index)
         else:
             out.mask = None
         out.table, out.lens, out.free_pages, out.max_new = table, lens, free_pages, int(max_new)
-    _launch("sparse_attn_cache_plan", dev, lib.sparse_attn_cache_plan, lens.data_ptr(), new_tokens.data_ptr(),
-            held.data_ptr(), nfree.data_ptr(), free_pages.data_ptr(), table.data_ptr(),
-            None if parents is None else parents.data_ptr(), R, free_pages.shape[0], int(page_size), width, n, mask_words,
-            out.held.data_ptr(), out.nfree.data_ptr(), out.starts.data_ptr(), out.granted.data_ptr(),
-            out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if mask_words else None)
+    _launch("sparse_attn_cache_plan", index, lib.sparse_attn_cache_plan, *ins, tree, R, free_pages.shape[0],
+            int(page_size), width, n, mask_words, out.held.data_ptr(), out.nfree.data_ptr(), out.starts.data_ptr(),
+            out.granted.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+            out.mask.data_ptr() if mask_words else None)
     return out
 
 
@@ -209,27 +208,26 @@ def sparse_attn_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tenso
     k and v may be strided with d contiguous (one layout for both), e.g. a transposed
     [Hkv, n, d] or a part of a fused projection. Slots other than -1 must differ."""
     lib = _lib.load()
-    c = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    _rows("k", k, k_cache.dtype, dev)
-    _rows("v", v, k_cache.dtype, dev)
-    n = k.shape[0]
-    if k.shape[1:] != (c.Hkv, c.d) or v.shape != k.shape:
+    c, kc, vc, index = _cache(k_cache, v_cache)
+    dtype, shape = k_cache.dtype, k.shape
+    kp, vp = _rows("k", k, dtype, index), _rows("v", v, dtype, index)
+    n = shape[0]
+    if shape[1:] != k_cache.shape[2:] or v.shape != shape:
         raise ValueError(f"k and v must be [n, {c.Hkv}, {c.d}]")
     if not _same_layout(k, v):
         raise ValueError("k and v must have the same strides")
-    _ints("slots", slots, (n,), dev)
+    at = _ints("slots", slots, (n,), index)
     if n == 0:
         return
-    _launch("sparse_attn_cache_write", dev, lib.sparse_attn_cache_write, k.data_ptr(), v.data_ptr(), k.stride(0),
-            k.stride(1), n, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), c)
+    tok, head, _ = k.stride()
+    _launch("sparse_attn_cache_write", index, lib.sparse_attn_cache_write, kp, vp, tok, head, n, at, kc, vc, c)
 
 
 def sparse_attn_tree_workspace_size(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                     plan: CachePlan) -> int:
     """Bytes of workspace sparse_attn_tree_fwd needs for these tensors."""
-    c = _cache(k_cache, v_cache)
-    return int(_lib.load().sparse_attn_tree_workspace_size(c, _step(plan, q.shape[0], k_cache.device), q.shape[1]))
+    c, _, _, index = _cache(k_cache, v_cache)
+    return int(_lib.load().sparse_attn_tree_workspace_size(c, _step(plan, q.shape[0], index), q.shape[1]))
 
 
 def sparse_attn_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, plan: CachePlan,
@@ -245,34 +243,35 @@ def sparse_attn_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     strided as q may. Rows of tokens that do not exist keep what `out` held (they are
     undefined in a new one); a row that sees nothing is 0."""
     lib = _lib.load()
-    c = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    _rows("q", q, k_cache.dtype, dev)
-    n, Hq, d = q.shape
-    if d != c.d or Hq < 1 or Hq % c.Hkv:
+    c, kc, vc, index = _cache(k_cache, v_cache)
+    dtype, shape = k_cache.dtype, q.shape
+    qp = _rows("q", q, dtype, index)
+    n, Hq, d = shape
+    if d != k_cache.shape[3] or Hq < 1 or Hq % k_cache.shape[2]:
         raise ValueError("q must be [n, Hq, d] with the cache's d and Hq a multiple of its heads")
     if out is None:
-        out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+        out = q.new_empty(shape)
+        op = out.data_ptr()
     else:
-        _rows("out", out, q.dtype, dev)
-        if out.shape != q.shape:
+        op = _rows("out", out, dtype, index)
+        if out.shape != shape:
             raise ValueError("out must have q's shape")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, Hq) or lse.device != dev
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, Hq) or lse.get_device() != index
                             or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [n, Hq] on q's device")
-    s = _step(plan, n, dev)
+    s = _step(plan, n, index)
     if n == 0:
         return out
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = torch.empty(int(lib.sparse_attn_tree_workspace_size(c, s, Hq)), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
+        workspace = q.new_empty(lib.sparse_attn_tree_workspace_size(c, s, Hq), dtype=torch.uint8)
+    elif workspace.get_device() != index:
         raise ValueError("workspace must be on q's device")
-    _launch("sparse_attn_tree_fwd", dev, lib.sparse_attn_tree_fwd, q.data_ptr(), q.stride(0), q.stride(1), Hq,
-            k_cache.data_ptr(), v_cache.data_ptr(), c, s, float(scale), out.data_ptr(), out.stride(0), out.stride(1),
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    q_tok, q_head, _ = q.stride()
+    o_tok, o_head, _ = out.stride()
+    _launch("sparse_attn_tree_fwd", index, lib.sparse_attn_tree_fwd, qp, q_tok, q_head, Hq, kc, vc, c, s, float(scale), op,
+            o_tok, o_head, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -284,15 +283,13 @@ def sparse_attn_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, plan:
     ([pages, page_size, Hkv, d]) or all layers' ([layers, ...]). The requests' lengths
     grow by `taken` (the caller adds it to lens)."""
     lib = _lib.load()
-    layers, layer_stride = 1, 0
+    layers, layer_stride, dims = 1, 0, 4
     if k_cache.dim() == 5:
-        layers, layer_stride = k_cache.shape[0], k_cache.stride(0)
-    c = _cache(k_cache, v_cache, k_cache.dim() if k_cache.dim() == 5 else 4)
-    dev = k_cache.device
-    s = _step(plan, 1, dev, masked=False)        # the moves read no row of the step's buffers
+        layers, layer_stride, dims = k_cache.shape[0], k_cache.stride(0), 5
+    c, kc, vc, index = _cache(k_cache, v_cache, dims)
+    s = _step(plan, 1, index, masked=False)      # the moves read no row of the step's buffers
     if accepted.dim() != 2 or accepted.shape[1] < 1:
         raise ValueError("accepted must be [R, cols]")
-    _ints("accepted", accepted, (s.R, accepted.shape[1]), dev)
-    _ints("taken", taken, (s.R,), dev)
-    _launch("sparse_attn_cache_accept", dev, lib.sparse_attn_cache_accept, k_cache.data_ptr(), v_cache.data_ptr(), c,
-            layers, layer_stride, s, accepted.data_ptr(), accepted.shape[1], taken.data_ptr())
+    R, cols = s.R, accepted.shape[1]
+    _launch("sparse_attn_cache_accept", index, lib.sparse_attn_cache_accept, kc, vc, c, layers, layer_stride, s,
+            _ints("accepted", accepted, (R, cols), index), cols, _ints("taken", taken, (R,), index))
