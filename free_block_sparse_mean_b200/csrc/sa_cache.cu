@@ -19,7 +19,11 @@ namespace {
 
 constexpr int kSMs = 148;                       // B200
 constexpr int64_t kMaxPlaces = 0x7fffffff - 1024;   // places of a request: the sums of one and a block stay ints
-constexpr int kTreeMinCost = 3;                 // smallest share of a CTA, in 64-key blocks
+// What a tile of one or two chains costs its CTA beside its blocks, in blocks: Q's load, the pass
+// of O out of TMEM (256 rows: 4 us). 64 ragged requests of up to 1,000 tokens, us: 51 for 0, 35.6
+// for 2, 35.1 for 3, 35.4 for 4; a prompt of 2,048 tokens: 84 for 2, 74 for 4, 70 for 6, 69 for 9;
+// 16 x 64 drafts: 193, 181, 176, 177.
+constexpr int kTileCost1 = 3, kTileCost2 = 6;
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
@@ -319,7 +323,8 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
   a.G = L.G;
   a.TT = L.chains * L.TC;
   a.TC = L.TC;
-  a.min_cost = kTreeMinCost;
+  a.tile_cost = L.chains == 2 ? kTileCost2 : kTileCost1;
+  a.min_cost = a.tile_cost + 1;
   a.O = O;
   a.o_token = s.n > 1 ? o_token : 0;
   a.o_head = Hq > 1 ? o_head : 0;

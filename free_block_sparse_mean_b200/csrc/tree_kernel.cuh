@@ -128,6 +128,7 @@ struct TreeArgs {
   const uint32_t* mask;           // [n][words] or null
   int R, n, width, pages, page_shift, words;
   int Hkv, G, TT, TC;             // key heads, query heads each, tokens of a tile, of a chain's part of it
+  int tile_cost;                  // what a tile costs beside its blocks, in blocks
   int min_cost;                   // smallest share of a CTA
   void* O;
   long long o_token, o_head;      // strides in elements
@@ -198,18 +199,13 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
   return sum;
 }
 
-// What a tile costs beside its blocks, in blocks: Q's load, the pass of O out of TMEM.
-// Without it 64 ragged requests of up to 1,000 tokens (512 tiles of 1 to 16 blocks) took
-// their CTAs between 22 and 42 us.
-constexpr int kTileCost = 2;
-
-// Cost of a key head's first `tiles` tiles of a request: their blocks and kTileCost each.
-__device__ __forceinline__ long long tree_cost_before(const TreeReq& q, int tiles, int TT, bool masked) {
+// Cost of a key head's first `tiles` tiles of a request: their blocks and tile_cost each.
+__device__ __forceinline__ long long tree_cost_before(const TreeReq& q, int tiles, const TreeArgs& a) {
   if (tiles <= 0) return 0;
-  const long long own = static_cast<long long>(tiles) * kTileCost;
-  if (masked) return static_cast<long long>(tiles) * q.nb + own;
+  const long long own = static_cast<long long>(tiles) * a.tile_cost;
+  if (a.mask != nullptr) return static_cast<long long>(tiles) * q.nb + own;
   const int full = min(tiles, q.tiles - 1);            // the last tile may hold fewer tokens
-  const long long s = full > 0 ? floor_sum(full, kBlock, TT, q.L + TT + kBlock - 1) : 0;
+  const long long s = full > 0 ? floor_sum(full, kBlock, a.TT, q.L + a.TT + kBlock - 1) : 0;
   return (tiles == q.tiles ? s + q.nb : s) + own;
 }
 
@@ -348,8 +344,10 @@ struct TreeWalk {
     nbt = tree_tile_blocks(q, tile, a.TT, a.mask != nullptr);
     n = static_cast<int>(min(left, static_cast<long long>(nbt - b0)));
   }
-  __device__ __forceinline__ long long after() const { return left - n - (b0 + n == nbt ? kTileCost : 0); }
-  __device__ __forceinline__ bool last() const { return after() <= 0 && kr < 0; }
+  __device__ __forceinline__ long long after(const TreeArgs& a) const {
+    return left - n - (b0 + n == nbt ? a.tile_cost : 0);
+  }
+  __device__ __forceinline__ bool last(const TreeArgs& a) const { return after(a) <= 0 && kr < 0; }
   // The first piece, from the share's first place: `at` in its tile (r, head, tile, q and
   // left set). False if the share holds no block.
   __device__ __forceinline__ bool begin(const TreeArgs& a, int at) {
@@ -363,7 +361,7 @@ struct TreeWalk {
     }
     b0 = at;
     cut(a);
-    if (b0 > 0 && after() > 0) {
+    if (b0 > 0 && after(a) > 0) {
       const int first = r;
       khead = head;
       ktile = tile;
@@ -375,7 +373,7 @@ struct TreeWalk {
   }
   // To the next piece of the share; false at its end.
   __device__ __forceinline__ bool next(const TreeArgs& a) {
-    left = after();
+    left = after(a);
     bool bad;
     if (left <= 0) {
       if (kr < 0) return false;
@@ -510,7 +508,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
   const int per = (a.R + C::kThreads - 1) / C::kThreads, r0 = static_cast<int>(threadIdx.x) * per;
   for (int r = r0; r < min(r0 + per, a.R); ++r) {
     mine = tree_request(a, r, &bad);
-    per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
+    per_head = tree_cost_before(mine, mine.tiles, a);
     cost += per_head * a.Hkv;
   }
   long long upto = cost, all = 0;             // of the requests up to the thread's last, of all
@@ -538,7 +536,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     if (per > 1) {
       for (;; ++r) {
         mine = tree_request(a, r, &bad);
-        per_head = tree_cost_before(mine, mine.tiles, a.TT, masked);
+        per_head = tree_cost_before(mine, mine.tiles, a);
         if (share0 < at + per_head * a.Hkv || r + 1 >= min(r0 + per, a.R)) break;
         at += per_head * a.Hkv;
       }
@@ -628,7 +626,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     int lo = 0, hi = w.q.tiles;                   // the last tile that begins at or before x
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      const long long v = tree_cost_before(w.q, mid, a.TT, masked);
+      const long long v = tree_cost_before(w.q, mid, a);
       if (v <= x) {
         lo = mid;
         at_tile = v;
@@ -663,7 +661,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         p->b0 = w.b0;
         p->n = w.n;
         p->nbt = w.nbt;
-        p->last = w.last();
+        p->last = w.last(a);
         p->special = 0;
         if (w.b0 == 0 && w.n < w.nbt)             // (its blocks are the share's last)
           a.cut[cta] = make_int4(p->tok0 + p->tile * a.TT, min(a.TT, p->T - p->tile * a.TT) * a.G, p->head,
