@@ -179,22 +179,24 @@ __device__ __forceinline__ long long div64(long long a, long long b) {
   return a / b;
 }
 
-// sum of floor((a i + b) / m) over i = 0 .. n-1 (a, b >= 0, m > 0), by the Euclidean
-// reduction: take whole parts out of a and b, then count the lattice points the other way.
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long sum = 0;
-  while (n > 0) {
-    const long long qa = div64(a, m), qb = div64(b, m);
-    sum += (n - 1) * n / 2 * qa + n * qb;
-    a -= qa * m;
-    b -= qb * m;
-    const long long y = a * n + b;
-    if (y < m) break;
+// sum of floor((a i + b) / 64) over i = 0 .. n-1 (a, b >= 0), by the Euclidean reduction:
+// take whole parts out of a and b, then count the lattice points the other way. Tiles of
+// whole blocks (a a multiple of 64) are done after the first step, which needs no division.
+__device__ __forceinline__ long long floor_sum64(long long n, int a0, int b0) {
+  static_assert(kBlock == 64, "shifts below");
+  long long sum = (n - 1) * n / 2 * (a0 >> 6) + n * (b0 >> 6);
+  long long a = a0 & 63, b = b0 & 63, m = 64, y = a * n + b;
+  while (y >= m) {
     n = div64(y, m);
     b = y - n * m;
     const long long t = m;
     m = a;
     a = t;
+    const long long qa = div64(a, m), qb = div64(b, m);
+    sum += (n - 1) * n / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    y = a * n + b;
   }
   return sum;
 }
@@ -205,7 +207,7 @@ __device__ __forceinline__ long long tree_cost_before(const TreeReq& q, int tile
   const long long own = static_cast<long long>(tiles) * a.tile_cost;
   if (a.mask != nullptr) return static_cast<long long>(tiles) * q.nb + own;
   const int full = min(tiles, q.tiles - 1);            // the last tile may hold fewer tokens
-  const long long s = full > 0 ? floor_sum(full, kBlock, a.TT, q.L + a.TT + kBlock - 1) : 0;
+  const long long s = full > 0 ? floor_sum64(full, a.TT, q.L + a.TT + kBlock - 1) : 0;
   return (tiles == q.tiles ? s + q.nb : s) + own;
 }
 
