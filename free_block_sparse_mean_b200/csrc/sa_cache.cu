@@ -164,7 +164,8 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
     cfg.gridDim = dim3(L.ctas, (rows + per - 1) / per);
     cfg.blockDim = dim3(32 * sa::kCombineWarps);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, sa::tree_combine_kernel<D, kElem>, a, per) != cudaSuccess) return SA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, sa::tree_combine_kernel<D, kElem, NC == 2 ? 2 : 4>, a, per) != cudaSuccess)
+      return SA_ERR_CUDA;
   }
   return SA_OK;
 }

@@ -1148,10 +1148,14 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
 // take one row after another, each every eighth piece; sums in a fixed order either way.
 // Looking for cut tiles from every (token, head) took 89 us for a prompt's chunk of
 // 4,096 x 32 rows of which 148 x 256 are cut; this takes 9.
+// kBatch: pieces that a warp reads at once. Tiles of two chains have many rows in two or three
+// pieces: two, in the registers that let an SM hold all its warps (3 x 500 new tokens behind
+// 1,000, the whole call: 54 us for four, 50 for two). Others have few rows, in up to 296 pieces:
+// four (7 x 13 drafts 18.2 us, for two 20.3).
 constexpr int kCombineWarps = 8;
 
-template <int D, int kElem>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+template <int D, int kElem, int kBatch>
+__global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 1)
     tree_combine_kernel(const __grid_constant__ TreeArgs a, int rows_per_block) {
   constexpr int kPer = D / 32;                      // elements of a lane
   __shared__ float s_o[kCombineWarps][D];
@@ -1177,7 +1181,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
 #pragma unroll
       for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * w0 + v[x] * w1;
     };
-    constexpr int kBatch = 4;                       // pieces read at once
     for (int p0 = shared ? warp : 0; p0 < np; p0 += kBatch * step) {
       float2 ml[kBatch];
       float v[kBatch][kPer];
