@@ -52,14 +52,15 @@
 // behind its barrier.
 //
 // Measured (one B200, bf16 unless said, in a captured graph): 64 requests of 1..16,384
-// cached tokens, 32 / 8 heads of 128, one token each, fp16: 334 us, 2.2 GB, the copy rate;
+// cached tokens, 32 / 8 heads of 128, one token each, fp16: 332 us, 2.2 GB, the copy rate;
 // one request of 4,096, 24 heads: 16 us for 50 MB, bound by its chain of set-up, load,
-// softmax, join; 16 requests x 64 drafted tokens: 188 us, 586 MB and 145 GFLOP; two chunks of
-// 2,048 tokens behind 30,000 and 7,080: 1,246 us, 1,054 TFLOP/s, bound by the chain of a
-// block's softmax and products at the power limit's clock. Tried and slower or no different:
-// chains taking turns at the exponentials (1,404 us), a part of them as polynomials on
-// the FMA pipe (1,406 to 1,469 for one in eight to one in two), exponentials ahead of the
-// block's maximum (1,441), registers split by setmaxnreg (spills).
+// softmax, join; 16 requests x 64 drafted tokens: 153 us, 586 MB and 145 GFLOP; two chunks of
+// 2,048 tokens behind 30,000 and 7,080: 1,113 us, 1,180 TFLOP/s, bound by the chain of a
+// block's softmax and products (in a long loop 1,247 us, at the power limit's clock). Tried and
+// slower or no different, against 1,238 to 1,322 us for the chunks: chains taking turns at the
+// exponentials (1,404), a part of them as polynomials on the FMA pipe (1,406 to 1,469 for
+// one in eight to one in two), exponentials ahead of the block's maximum (1,441), registers
+// split by setmaxnreg (spills).
 #pragma once
 
 #include <cuda_fp16.h>
