@@ -47,8 +47,9 @@ class CachePlan:
     held       int32 [R]         pages in each table row, for the next step
     nfree      int32 [1]         ids on the free list, for the next step
     free_pages int32 [pages]     the free list
-    max_new    int               the most new tokens of a request if known (0: not known);
-                                 only sizes the attention's tiles
+    max_new    int               the most new tokens of a request if known (0: not known, about
+                                 the mean); only sizes the attention's tiles, so it is worth
+                                 giving where requests differ much
     """
     table: torch.Tensor
     lens: torch.Tensor

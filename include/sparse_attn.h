@@ -405,8 +405,8 @@ typedef struct {
   int32_t R;               /* requests, 1..8192 */
   int32_t n;               /* rows of the step's token buffers */
   int32_t width;           /* columns of table; R*width, width*page_size <= 2^31 - 1025 */
-  int32_t max_new;         /* the most new tokens of a request, or 0 if not known. It only
-                              sizes the tiles: more tokens than this are still right */
+  int32_t max_new;         /* the most new tokens of a request, or 0 if not known (then n / R is
+                              taken). It only sizes the tiles: more tokens are still right */
   int32_t words;           /* words of a mask row, 1..32, or 0 with mask = NULL */
   const int32_t* starts;   /* [R+1]: request r's new tokens are rows starts[r]..starts[r+1]-1 */
   const int32_t* lens;     /* [R]: its tokens in the cache before them */

@@ -81,6 +81,12 @@ def test_masks_and_workspaces_that_do_not_fit():
         chains = 2 if new * hq // 2 > rows else 1
         assert size >= 2 * (296 // chains) * chains * rows * (64 * 4 + 8)
         assert tree(s=s, Hq=hq, q_token=64 * hq, o_token=64 * hq, ws_bytes=size - 1) == WORKSPACE
+    # without max_new the mean sizes the tiles, at least 32 rows; a mask's words bound them
+    size = lambda **kw: lib.sparse_attn_tree_workspace_size(cache(), step(width=100, **kw), 8)      # 4 heads to a key head
+    assert size(R=64, n=64, max_new=0) == size(R=64, n=64, max_new=8)
+    assert size(R=4, n=200, max_new=0) == size(R=4, n=200, max_new=50)
+    assert size(R=1, n=5, max_new=0) == size(R=1, n=5, max_new=5)
+    assert size(R=1, n=64, max_new=0, mask=P, words=1) == size(R=1, n=64, max_new=32)
     # a request of one block is never cut
     assert lib.sparse_attn_tree_workspace_size(cache(), step(width=4), 4) == 256
 
