@@ -482,6 +482,8 @@ sa_status sparse_attn_cache_write(const void* K, const void* V, int64_t token_st
  * cached pages behind a request's last token, and keys and values of new tokens in rows
  * that do not see them, never reach a result, infinities and NaN included. A request with
  * counts out of range is skipped (bit 2); a page id out of range is read as page 0 (bit 1).
+ * Requests may share pages (a common prefix). The call's kernels may set themselves up while
+ * what is before them in the stream ends; they wait for it before they read or write memory.
  * Results do not depend on timing; the number of pieces a row's keys are cut into, and so
  * the rounding, depends on the lengths of all requests of the call. Errors: as
  * sparse_attn_fwd, and SA_ERR_WORKSPACE. */
