@@ -68,17 +68,18 @@ class CachePlan:
 # not its kernels (a plan of 64 requests 4 us of 18), and a check that passes is one
 # expression. What it refuses is looked at again for the message.
 _I32 = torch.int32
-_get_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _launch(name: str, index: int, call, *args):
-    """The C call on the GPU's current torch stream (no device switch if it is the current one)."""
-    if _get_device() == index:
-        st = call(*args, _raw_stream(index))
+    """The C call on the GPU's current torch stream (no device switch if it is the current one).
+    torch._C's functions spare the host what torch.cuda's wrap around them; a torch without CUDA
+    does not have them, so they are looked up here and not at import."""
+    c = torch._C
+    if c._cuda_getDevice() == index:
+        st = call(*args, c._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = call(*args, _raw_stream(index))
+            st = call(*args, c._cuda_getCurrentRawStream(index))
     if st != _lib.SA_OK:
         raise SparseAttnError(name, st, _lib.load())
 
