@@ -917,6 +917,13 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
     p_full += 2 * c;
     pv_done += 2 * c;
     const int row = wq * C::kWarpRows + lane;
+    // P = 2^(s - m_ref) is rounded to the type: that is what the tensor cores multiply V with
+    // (two products, of P's head and rest, would be half as many again). bf16 has fp32's range.
+    // fp16 holds 2^-24 to 2^16: its reference is 2^6 below the maximum it was taken from, so
+    // that P stays below 2^12 (2^14 with scores up to 2^26, whose own steps are 4) and a key is
+    // only lost below 2^-31 of the row's largest probability. With the maximum itself as reference
+    // that was 2^-25: 100,000 such keys behind one peak weigh 3e-3, six roundings of the result.
+    constexpr float kRefBelow = kElem == kElemF16 ? 6.f : 0.f, kRefGrowth = kElem == kElemF16 ? 12.f : 8.f;
     bool alive = true;
     int k = 0;                                     // blocks of the chain
     for (int item = 0; alive; ++item) {
@@ -979,13 +986,14 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
         for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], s1[u + 24]);
         const float rmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
                            a.scale_log2;
-        // the reference maximum is raised only when a row's maximum grows by more
-        // than 2^8: P stays below 2^8 (in range of both types), O and l unchanged
-        const bool raise = rmax > m_ref + 8.f;
+        // the reference is raised only when a row's maximum has grown by more than
+        // 2^8 (fp16: 2^6), so that O and l are seldom corrected; see kRefBelow
+        const bool raise = rmax > m_ref + kRefGrowth;
         float alpha = 1.f;
         if (raise) {
-          alpha = ex2(m_ref - rmax);
-          m_ref = rmax;
+          const float m_new = rmax - kRefBelow;
+          alpha = ex2(m_ref - m_new);
+          m_ref = m_new;
         }
         const bool any_raise = __any_sync(FULL, raise);
         const float mref = (m_ref == -INFINITY) ? 0.f : m_ref;

@@ -468,7 +468,9 @@ sa_status sparse_attn_cache_write(const void* K, const void* V, int64_t token_st
  * head h / (Hq/Hkv)), O[i][h] = softmax over the request's cached tokens and the new
  * ones that i sees of scale * q.k, times V. The new tokens' keys and values are in the
  * cache already (sparse_attn_cache_write). Scores, softmax and sums are fp32; P is
- * rounded to the type for P.V.
+ * rounded to the type for P.V. In fp16 a key of less than 2^-31 of its row's largest
+ * probability is lost by that (bf16 has the range of fp32), and |scale q.k| above 4e7 may
+ * overflow it.
  *
  *   Q, O       [n][Hq][d] with their strides (elements, multiples of 8), Hq a multiple of
  *              c.Hkv, at most 128 query heads to a key head

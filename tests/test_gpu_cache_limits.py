@@ -1,0 +1,75 @@
+"""Paged cache at the limits its calls state: probabilities far below a row's largest, sizes
+and counts at the ends of their ranges, numbers out of range."""
+import math
+
+import pytest
+import torch
+
+from oracle import paged_cache_oracle as orc
+from tests.test_gpu_cache import BF, HF, cache_of, dev_ints, no_device_error
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import free_block_sparse_mean_b200 as sa
+
+
+@pytest.mark.parametrize("R,T,ctx,peak", [(1, 1, 30000, 17001), (300, 1, 12000, 5), (300, 1, 12000, 11990),
+                                          (300, 40, 3000, 1501), (150, 90, 3000, 64)])
+@pytest.mark.parametrize("gap", [17.5, 19.0, 20.5])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_many_small_probabilities_behind_one_peak(R, T, ctx, peak, gap, dtype):
+    """A key that takes nearly all of the softmax and has V = 0, `gap` nats above all others:
+    what they hold together is the result. e^-20.5 is 2^-29.6 of the largest probability. R
+    requests read one request's pages, so many that most rows are in one piece.
+
+    Bound: u a for P, u |o| for the result (u half a step), as every row's (2^-22 for ex2 and
+    (d + 3) 2^-23 of sum |q||k| for a score, twice; fp32 sums keys 2^-23). In fp16 also 2^-31 of
+    the largest V for each key (P is rounded by 2^-25 at most below 2^-14, the row's sum is 2^6
+    or more) and 2^-25 of a result below 2^-14."""
+    d, page = 64, 64
+    g = torch.Generator().manual_seed(T)
+    kc, vc, table = cache_of([ctx], [T], page, 1, d, dtype, T, fill=0.0)
+    q = torch.zeros(T, 1, d, dtype=dtype)
+    q[:, :, 0] = 1.0
+    flat = torch.zeros(ctx + T, 1, d, dtype=dtype)
+    flat[:, :, 0] = (-gap + 0.25 * torch.rand(ctx + T, 1, generator=g)).to(dtype)
+    flat[peak, :, 0] = 0.0
+    val = (0.5 + torch.rand(ctx + T, 1, d, generator=g)).to(dtype)
+    val[peak] = 0.0
+    at = torch.arange(ctx + T)
+    ids = torch.tensor(table[0])[at // page].long()
+    kc[ids, at % page], vc[ids, at % page] = flat, val
+    plan = sa.CachePlan(table=dev_ints(table * R), lens=dev_ints([ctx] * R),
+                        starts=dev_ints([T * r for r in range(R + 1)]), max_new=T)
+    lse = torch.empty(R * T, 1, device="cuda")
+    got = sa.sparse_attn_tree_fwd(q.cuda().repeat(R, 1, 1), kc.cuda(), vc.cuda(), plan, 1.0, lse=lse).cpu().double()
+    no_device_error()
+    o, ref_lse, a, smax = orc.tree_attention(q, kc, vc, table, [ctx], [0, T], [T], None, 1.0)
+    u = torch.finfo(dtype).eps / 2
+    e = (d + 3) * 2.0 ** -23 * smax[..., None] + 2.0 ** -22
+    keys = ctx + T
+    tol = u * a * (1 + u) + u * (o.abs() + u * a) + 2 * e * a + keys * 2.0 ** -23 * a
+    if dtype == HF:
+        tol = tol + keys * 2.0 ** -31 * 1.5 + 2.0 ** -25
+    err = (got.view(R, T, 1, d) - o).abs()
+    assert torch.all(err <= tol), f"worst {float((err / tol).max()):.2f} of the bound"
+    e = (d + 3) * 2.0 ** -23 * smax + (keys + 8) * 2.0 ** -23 + 2.0 ** -22 * ref_lse.abs()
+    assert torch.all((lse.cpu().double().view(R, T, 1) - ref_lse).abs() <= e)
+
+
+@pytest.mark.parametrize("size", [40.0, 3000.0, 10000.0])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_scores_of_any_size_stay_finite(size, dtype):
+    """Scores whose steps in fp32 pass those of the exponent (up to 2e7): no infinity or NaN,
+    and every row within the range of its values."""
+    ctx, T, page, d = 700, 5, 32, 64
+    kc, vc, table = cache_of([ctx], [T], page, 1, d, dtype, 3)
+    kc = (kc.float() * 40).to(dtype)
+    q = (torch.randn(T, 2, d, generator=torch.Generator().manual_seed(1)) * size).to(dtype)
+    plan = sa.CachePlan(table=dev_ints(table), lens=dev_ints([ctx]), starts=dev_ints([0, T]), max_new=T)
+    lse = torch.empty(T, 2, device="cuda")
+    got = sa.sparse_attn_tree_fwd(q.cuda(), kc.cuda(), vc.cuda(), plan, 1.0, lse=lse)
+    no_device_error()
+    assert torch.isfinite(got).all() and torch.isfinite(lse).all()
+    assert float(got.float().abs().max()) <= float(vc.float().abs().max()) * 1.01
