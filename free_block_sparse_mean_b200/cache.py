@@ -289,7 +289,10 @@ def sparse_attn_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, plan:
     if k_cache.dim() == 5:
         layers, layer_stride, dims = k_cache.shape[0], k_cache.stride(0), 5
     c, kc, vc, index = _cache(k_cache, v_cache, dims)
-    s = _step(plan, 1, index, masked=False)      # the moves read no row of the step's buffers
+    # rows that a request claims past the step's buffers are refused as in the attention; a plan
+    # put together without them has no number to check
+    rows = plan.slots if plan.slots is not None else plan.mask
+    s = _step(plan, 0x7fffffff if rows is None else rows.shape[0], index, masked=False)
     if accepted.dim() != 2 or accepted.shape[1] < 1:
         raise ValueError("accepted must be [R, cols]")
     R, cols = s.R, accepted.shape[1]

@@ -328,21 +328,23 @@ struct CacheAcceptArgs {
   uint4* cache[2];
   const int *lens, *starts, *granted, *table, *accepted, *taken;
   long long layer, page_stride, token, head;     // strides in 16-byte pieces
-  int R, width, cols, pages, page_shift, vecs, H, layers, n;
+  int width, cols, pages, page_shift, vecs, H, layers, n;
 };
 
 constexpr int kAcceptMax = 1024;   // accepted tokens of one request
 
-__global__ void __launch_bounds__(256) cache_accept_kernel(const CacheAcceptArgs a) {
+__global__ void __launch_bounds__(256, 4) cache_accept_kernel(const CacheAcceptArgs a) {
   __shared__ long long s_src[kAcceptMax], s_dst[kAcceptMax];
   const int r = blockIdx.x;
   const int m = a.taken[r];
-  const int T0 = a.starts[r + 1] - a.starts[r];
+  const int s0 = a.starts[r], s1 = a.starts[r + 1];
+  const bool rows_ok = s0 >= 0 && s1 >= s0 && s1 <= a.n;
+  const int T0 = rows_ok ? s1 - s0 : 0;
   const int T = a.granted ? min(T0, a.granted[r]) : T0;
   const int L = a.lens[r];
   const int page = 1 << a.page_shift;
   int err = 0;
-  if (m < 0 || m > a.cols || m > max(T, 0) || L < 0 ||
+  if (!rows_ok || m < 0 || m > a.cols || m > max(T, 0) || L < 0 ||
       static_cast<long long>(L) + max(T, 0) > static_cast<long long>(a.width) * page)
     err = DEVERR_VALUE;
   int first = 0x7fffffff;                        // the first token that moves
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(256) cache_accept_kernel(const CacheAcceptArgs
     const int head = static_cast<int>(q % a.H);
     q /= a.H;
     const int layer = static_cast<int>(q >> 1);
-    uint4* base = a.cache[q & 1] + layer * a.layer + head * a.head + vec;
+    uint4* base = (q & 1 ? a.cache[1] : a.cache[0]) + layer * a.layer + head * a.head + vec;   // (as in the write)
     for (int i0 = first; i0 < m; i0 += 8) {
       uint4 v[8];
 #pragma unroll

@@ -381,7 +381,6 @@ sa_status sparse_attn_cache_accept(void* K_cache, void* V_cache, sa_cache c, int
   a.page_stride = c.page_stride / 8;
   a.token = c.token_stride / 8;
   a.head = c.Hkv > 1 ? c.head_stride / 8 : 0;
-  a.R = s.R;
   a.n = s.n;
   a.width = s.width;
   a.cols = cols;

@@ -499,7 +499,8 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
  * for i < taken[r], in every layer (layer l's caches lie l*layer_stride elements behind the
  * bases). accepted is [R][cols], a[0] < a[1] < ... < the request's new tokens, cols <=
  * 1024; 0 <= taken[r] <= cols. The new length of the request is lens[r] + taken[r]. A
- * request whose numbers are out of range keeps its rows and sets bit 2 (a page id: bit 1).
+ * request whose numbers are out of range (its rows past n among them) keeps its rows of the
+ * cache and sets bit 2 (a page id: bit 1).
  * The pages of two requests in one call must differ from place lens on. */
 sa_status sparse_attn_cache_accept(void* K_cache, void* V_cache, sa_cache c, int32_t layers, int64_t layer_stride,
                                    sa_step s, const int32_t* accepted, int32_t cols, const int32_t* taken,

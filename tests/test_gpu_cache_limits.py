@@ -73,3 +73,24 @@ def test_scores_of_any_size_stay_finite(size, dtype):
     no_device_error()
     assert torch.isfinite(got).all() and torch.isfinite(lse).all()
     assert float(got.float().abs().max()) <= float(vc.float().abs().max()) * 1.01
+
+
+@pytest.mark.parametrize("known", ["slots", "mask", None])
+def test_accept_refuses_rows_that_are_not_the_steps(known):
+    """Starts past the step's rows, negative or falling: the request keeps its rows and is
+    flagged, as the attention does. (Without slots and mask the number of rows is not known.)"""
+    n, R, T = 24, 3, 8
+    kc, vc, table = cache_of([20] * R, [T] * R, 16, 2, 64, BF, 4)
+    acc, taken = [[1, 3, 5]] * R, [3] * R
+    extra = {} if known is None else {known: dev_ints([0] * n) if known == "slots" else dev_ints([[0]] * n)}
+    for starts, moved, want in (([0, 8, 16, 24], [0, 1, 2], 0), ([0, 8, 16, 25], [0, 1] if known else [0, 1, 2], 4),
+                                ([-8, 0, 8, 16], [1, 2], 4), ([0, 8, 4, 16], [0, 2], 4)):
+        want = 0 if len(moved) == R else want
+        kg, vg = kc.cuda(), vc.cuda()
+        plan = sa.CachePlan(table=dev_ints(table), lens=dev_ints([20] * R), starts=dev_ints(starts), **extra)
+        sa.sparse_attn_cache_accept(kg, vg, plan, dev_ints(acc), dev_ints(taken))
+        torch.cuda.synchronize()
+        assert sa.sparse_attn_device_error() == want, starts
+        rows = [table[r] for r in moved]
+        assert torch.equal(kg.cpu(), orc.accept(kc, rows, [20] * len(moved), acc, taken)), starts
+        assert torch.equal(vg.cpu(), orc.accept(vc, rows, [20] * len(moved), acc, taken)), starts
