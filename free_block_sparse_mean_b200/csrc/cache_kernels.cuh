@@ -176,8 +176,9 @@ __global__ void __launch_bounds__(kCachePlanThreads) cache_plan_kernel(const Cac
     const int held = a.held[r];
     const long long row = static_cast<long long>(r) * a.width;
     if (back > 0) {
-      for (int j = lane; j < back; j += 32)
-        if (nfree + s_back[r] + j < a.pages) a.free_pages[nfree + s_back[r] + j] = a.table[row + j];
+      // what the list has room for (nfree + s_back[r] may pass 2^31 where counts are wrong)
+      const int fit = min(back, a.pages - nfree - min(s_back[r], a.pages - nfree));
+      for (int j = lane; j < fit; j += 32) a.free_pages[nfree + s_back[r] + j] = a.table[row + j];
     } else if (ok && need > 0) {
       for (int j = lane; j < need; j += 32) a.table[row + held + j] = list_at(top - 1 - (s_need[r] + j));
     }

@@ -94,3 +94,25 @@ def test_accept_refuses_rows_that_are_not_the_steps(known):
         rows = [table[r] for r in moved]
         assert torch.equal(kg.cpu(), orc.accept(kc, rows, [20] * len(moved), acc, taken)), starts
         assert torch.equal(vg.cpu(), orc.accept(vc, rows, [20] * len(moved), acc, taken)), starts
+
+
+def test_plan_returns_more_pages_than_ints_count():
+    """Ended requests that claim R * width pages, nearly 2^31, behind a full list: their sum and
+    the list's length pass 2^31. Nothing is written and the counts are flagged."""
+    R, pages = 8192, 100000
+    width = (2 ** 31 - 1) // R
+    assert R * width < 2 ** 31 < R * width + pages
+    table = torch.zeros(R, width, dtype=torch.int32, device="cuda")
+    free = torch.arange(pages, dtype=torch.int32, device="cuda")
+    guard = torch.full((R,), width, dtype=torch.int32, device="cuda")
+    p = sa.sparse_attn_cache_plan(dev_ints([0] * R), dev_ints([-1] * R), table, guard, free, dev_ints([pages]), 4, 16)
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_device_error() == 4
+    assert torch.equal(free, torch.arange(pages, dtype=torch.int32, device="cuda")) and int(p.nfree) == pages
+    # room for 7 more: the first request's pages fill the list
+    table[0, :8] = dev_ints([41, 42, 43, 44, 45, 46, 47, 48])
+    p = sa.sparse_attn_cache_plan(dev_ints([0] * R), dev_ints([-1] * R), table, guard, free, dev_ints([pages - 7]), 4, 16)
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_device_error() == 4
+    assert free[pages - 8:].tolist() == [pages - 8, 41, 42, 43, 44, 45, 46, 47] and int(p.nfree) == pages
+    assert p.granted.count_nonzero() == 0 and p.held.count_nonzero() == 0
