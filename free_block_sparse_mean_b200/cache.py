@@ -268,8 +268,8 @@ def sparse_attn_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         workspace = q.new_empty(lib.sparse_attn_tree_workspace_size(c, s, Hq), dtype=torch.uint8)
-    elif workspace.get_device() != index:
-        raise ValueError("workspace must be on q's device")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
     q_tok, q_head, _ = q.stride()
     o_tok, o_head, _ = out.stride()
     _launch("sparse_attn_tree_fwd", index, lib.sparse_attn_tree_fwd, qp, q_tok, q_head, Hq, kc, vc, c, s, float(scale), op,

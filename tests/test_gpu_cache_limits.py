@@ -116,3 +116,20 @@ def test_plan_returns_more_pages_than_ints_count():
     assert sa.sparse_attn_device_error() == 4
     assert free[pages - 8:].tolist() == [pages - 8, 41, 42, 43, 44, 45, 46, 47] and int(p.nfree) == pages
     assert p.granted.count_nonzero() == 0 and p.held.count_nonzero() == 0
+
+
+def test_a_workspace_that_is_a_view_of_less_memory_is_refused():
+    """A broadcast tensor's nbytes count the same bytes again and again."""
+    kc, vc, table = cache_of([100], [2], 16, 2, 64, BF, 4, fill=0.0)
+    kc, vc = kc.cuda(), vc.cuda()
+    plan = sa.CachePlan(table=dev_ints(table), lens=dev_ints([100]), starts=dev_ints([0, 2]))
+    q = torch.zeros(2, 4, 64, dtype=BF, device="cuda")
+    size = sa.sparse_attn_tree_workspace_size(q, kc, vc, plan)
+    byte = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for ws in (byte.expand(size), torch.zeros(size, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError):
+            sa.sparse_attn_tree_fwd(q, kc, vc, plan, workspace=ws)
+    want = sa.sparse_attn_tree_fwd(q, kc, vc, plan)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    assert torch.equal(sa.sparse_attn_tree_fwd(q, kc, vc, plan, workspace=ws), want)
+    no_device_error()
