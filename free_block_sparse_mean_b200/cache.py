@@ -110,6 +110,13 @@ def _strides(name: str, t: torch.Tensor):
     return ptr
 
 
+def _sizes(any_of: int):
+    """The C calls take sizes in 32 bits, and ctypes would drop the bits above: refuses the OR of
+    sizes of which one needs more. (Rows of heads do not fit into memory before that.)"""
+    if not -0x80000000 <= any_of <= 0x7fffffff:
+        raise ValueError("a size is out of range (2^31 or more)")
+
+
 def _same_layout(a: torch.Tensor, b: torch.Tensor) -> bool:
     x, y = a.stride(), b.stride()
     return x == y or all(i == j for i, j, e in zip(x, y, a.shape) if e > 1)
@@ -137,12 +144,14 @@ def _step(plan: CachePlan, n: int, index: int, masked: bool = True) -> SaStep:
     if table.dim() != 2:
         raise ValueError("the plan's table must be [R, width]")
     R, width = shape = table.shape
+    max_new = int(plan.max_new)
+    _sizes(R | n | width | max_new)
     if granted is not None:
         granted = _ints("the plan's granted", granted, (R,), index)
     if masked and plan.mask is not None:
         words = plan.mask.shape[-1]
         mask = _ints("the plan's mask", plan.mask, (n, words), index)
-    return SaStep(R, n, width, int(plan.max_new), words, _ints("the plan's starts", plan.starts, (R + 1,), index),
+    return SaStep(R, n, width, max_new, words, _ints("the plan's starts", plan.starts, (R + 1,), index),
                   _ints("the plan's lens", plan.lens, (R,), index), granted,
                   _ints("the plan's table", table, shape, index), mask)
 
@@ -170,7 +179,8 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
     vec = (R,)
     if free_pages.dim() != 1:
         raise ValueError("free_pages must be [pages]")
-    n, mask_words = int(n), int(mask_words)
+    n, mask_words, page_size, max_new = int(n), int(mask_words), int(page_size), int(max_new)
+    _sizes(R | width | free_pages.shape[0] | n | mask_words | page_size | max_new)
     if n < 1 or mask_words < 0:
         raise ValueError("n must be at least 1 and mask_words at least 0")
     ins = (_ints("lens", lens, vec, index), _ints("new_tokens", new_tokens, vec, index), _ints("held", held, vec, index),
@@ -186,7 +196,7 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
         starts, granted, held_out, nfree_out, slots, positions, mask = \
             lens.new_empty(sum(sizes)).split_with_sizes(sizes)
         out = CachePlan(table, lens, starts, granted, mask.view(n, mask_words) if mask_words else None, slots,
-                        positions, held_out, nfree_out, free_pages, int(max_new))
+                        positions, held_out, nfree_out, free_pages, max_new)
     else:
         for name, t, want in (("starts", out.starts, (R + 1,)), ("granted", out.granted, vec), ("slots", out.slots, (n,)),
                               ("positions", out.positions, (n,)), ("held", out.held, vec),
@@ -196,9 +206,9 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
             _ints("out.mask", out.mask, (n, mask_words), index)
         else:
             out.mask = None
-        out.table, out.lens, out.free_pages, out.max_new = table, lens, free_pages, int(max_new)
+        out.table, out.lens, out.free_pages, out.max_new = table, lens, free_pages, max_new
     _launch("sparse_attn_cache_plan", index, lib.sparse_attn_cache_plan, *ins, tree, R, free_pages.shape[0],
-            int(page_size), width, n, mask_words, out.held.data_ptr(), out.nfree.data_ptr(), out.starts.data_ptr(),
+            page_size, width, n, mask_words, out.held.data_ptr(), out.nfree.data_ptr(), out.starts.data_ptr(),
             out.granted.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
             out.mask.data_ptr() if mask_words else None)
     return out
@@ -296,5 +306,6 @@ def sparse_attn_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, plan:
     if accepted.dim() != 2 or accepted.shape[1] < 1:
         raise ValueError("accepted must be [R, cols]")
     R, cols = s.R, accepted.shape[1]
+    _sizes(cols)
     _launch("sparse_attn_cache_accept", index, lib.sparse_attn_cache_accept, kc, vc, c, layers, layer_stride, s,
             _ints("accepted", accepted, (R, cols), index), cols, _ints("taken", taken, (R,), index))

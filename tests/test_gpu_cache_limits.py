@@ -133,3 +133,23 @@ def test_a_workspace_that_is_a_view_of_less_memory_is_refused():
     ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     assert torch.equal(sa.sparse_attn_tree_fwd(q, kc, vc, plan, workspace=ws), want)
     no_device_error()
+
+
+def test_sizes_past_32_bits_are_refused():
+    """The C calls' sizes are 32 bits wide; ctypes drops what is above them without a word."""
+    one = dev_ints([1])
+    call = lambda n=4, page=16, **kw: sa.sparse_attn_cache_plan(dev_ints([0]), one, dev_ints([[0]]), dev_ints([0]),
+                                                                dev_ints([0]), one, n, page, **kw)
+    p = call()
+    # written again into buffers of 4 rows: a wide n must not be taken for its low bits
+    for kw in (dict(n=2 ** 32 + 4), dict(page=2 ** 32 + 16), dict(max_new=2 ** 32 + 1), dict(mask_words=2 ** 32)):
+        with pytest.raises(ValueError):
+            call(out=p if "page" in kw else None, **kw)
+    kc = torch.zeros(2, 16, 1, 64, dtype=BF, device="cuda")
+    p = call()
+    p.max_new = 2 ** 32 + 1
+    with pytest.raises(ValueError):
+        sa.sparse_attn_tree_fwd(torch.zeros(4, 1, 64, dtype=BF, device="cuda"), kc, kc.clone(), p)
+    p.max_new = 1
+    sa.sparse_attn_tree_fwd(torch.zeros(4, 1, 64, dtype=BF, device="cuda"), kc, kc.clone(), p)
+    no_device_error()
