@@ -219,8 +219,20 @@ sa_status launch_cluster(const sa_shape& s, const void* X, const void* Y, int it
 }  // namespace
 
 namespace sa {
-cudaError_t take_noalloc_device_error(cudaStream_t st, unsigned int* out);   // sa_noalloc.cu
-cudaError_t take_cache_device_error(cudaStream_t st, unsigned int* out);     // sa_cache.cu
+cudaError_t noalloc_device_error_word(void** word);   // sa_noalloc.cu
+cudaError_t cache_device_error_word(void** word);     // sa_cache.cu
+
+// Moves the codes of the other translation units' device error words into this one's.
+__global__ void __launch_bounds__(32) gather_device_errors_kernel(unsigned int* a, unsigned int* b) {
+  if (threadIdx.x == 0) {
+    const unsigned int codes = atomicExch(a, 0u) | atomicExch(b, 0u);
+    if (codes) atomicOr(&g_dev_error, codes);
+  }
+}
+// Takes codes that the host has read out of the word; others, set meanwhile, stay.
+__global__ void __launch_bounds__(32) clear_device_errors_kernel(unsigned int codes) {
+  if (threadIdx.x == 0) atomicAnd(&g_dev_error, ~codes);
+}
 
 // Exercises the device-side failure path: one warp waits on an mbarrier whose
 // phase nothing completes, through the same bounded wait the pipelines use, with
@@ -660,17 +672,23 @@ sa_status sparse_attn_selftest_wait_timeout(uint32_t limit_us, void* stream) {
 sa_status sparse_attn_device_error(void* stream, int32_t* code) {
   if (!code) return SA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int v = 0, zero = 0;
+  // One small launch and one copy, which waits; a second launch where a code is set. (A read,
+  // a clear and a wait for each translation unit's word took 50 us of the host for three of them, 22
+  // now, and lost a code that another stream's kernel set between the read and the clear.)
+  void *a = nullptr, *b = nullptr;
+  if (sa::noalloc_device_error_word(&a) != cudaSuccess || sa::cache_device_error_word(&b) != cudaSuccess)
+    return SA_ERR_CUDA;
+  sa::gather_device_errors_kernel<<<1, 32, 0, st>>>(static_cast<unsigned int*>(a), static_cast<unsigned int*>(b));
+  if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+  unsigned int v = 0;
   if (cudaMemcpyFromSymbolAsync(&v, sa::g_dev_error, sizeof(v), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess)
     return SA_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(sa::g_dev_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) !=
-      cudaSuccess)
-    return SA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return SA_ERR_CUDA;
-  unsigned int w = 0, x = 0;   // the other translation units' words (sa_noalloc.cu, sa_cache.cu)
-  if (sa::take_noalloc_device_error(st, &w) != cudaSuccess) return SA_ERR_CUDA;
-  if (sa::take_cache_device_error(st, &x) != cudaSuccess) return SA_ERR_CUDA;
-  *code = static_cast<int32_t>(v | w | x);
+  if (v) {
+    sa::clear_device_errors_kernel<<<1, 32, 0, st>>>(v);
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) return SA_ERR_CUDA;
+  }
+  *code = static_cast<int32_t>(v);
   return SA_OK;
 }
 

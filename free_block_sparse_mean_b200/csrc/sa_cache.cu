@@ -181,15 +181,8 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
 }  // namespace
 
 namespace sa {
-// Reads and clears this translation unit's device error word.
-cudaError_t take_cache_device_error(cudaStream_t st, unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_dev_error, sizeof(*out), 0, cudaMemcpyDeviceToHost, st);
-  if (e != cudaSuccess) return e;
-  e = cudaMemcpyToSymbolAsync(g_dev_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-  if (e != cudaSuccess) return e;
-  return cudaStreamSynchronize(st);
-}
+// The current GPU's copy of this translation unit's device error word.
+cudaError_t cache_device_error_word(void** word) { return cudaGetSymbolAddress(word, g_dev_error); }
 }  // namespace sa
 
 extern "C" {

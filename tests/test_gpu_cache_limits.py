@@ -1,6 +1,7 @@
 """Paged cache at the limits its calls state: probabilities far below a row's largest, sizes
 and counts at the ends of their ranges, numbers out of range."""
 import math
+import time
 
 import pytest
 import torch
@@ -153,3 +154,50 @@ def test_sizes_past_32_bits_are_refused():
     p.max_new = 1
     sa.sparse_attn_tree_fwd(torch.zeros(4, 1, 64, dtype=BF, device="cuda"), kc, kc.clone(), p)
     no_device_error()
+
+
+def out_of_pool(kc):
+    """Sets bit 1 through a write to a slot outside the pool."""
+    row = torch.ones(1, kc.shape[2], kc.shape[3], dtype=kc.dtype, device="cuda")
+    sa.sparse_attn_cache_write(row, row, dev_ints([kc.shape[0] * kc.shape[1]]), kc, kc.clone())
+
+
+def test_the_error_word_gathers_every_code_once():
+    """Codes of kernels of different translation units come back together and are cleared; one set
+    on another stream while the word is read is not lost."""
+    kc = torch.zeros(1, 16, 1, 64, dtype=BF, device="cuda")
+    no_device_error()
+    sa.sparse_attn_selftest_wait_timeout(1000)
+    out_of_pool(kc)
+    sa.sparse_attn_cache_plan(dev_ints([-1]), dev_ints([1]), dev_ints([[0]]), dev_ints([0]), dev_ints([0]), dev_ints([1]),
+                              1, 16)
+    assert sa.sparse_attn_device_error() == 7 and sa.sparse_attn_device_error() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(100):
+        with torch.cuda.stream(side):
+            out_of_pool(kc)
+        seen, stop = 0, time.monotonic() + 10
+        while not seen and time.monotonic() < stop:
+            seen = sa.sparse_attn_device_error()
+        assert seen == 2
+        torch.cuda.synchronize()
+        assert sa.sparse_attn_device_error() == 0
+
+
+def test_reading_the_error_word_is_a_launch_and_a_copy():
+    """sparse_attention reads the word in every call: 2.4 times the host time of a tensor's
+    item(), one small copy that waits. A read, a clear and a wait for each of the library's three
+    translation units were 5.5 times it."""
+    x = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def least(call):
+        best = math.inf
+        for _ in range(500):
+            t = time.perf_counter()
+            call()
+            best = min(best, time.perf_counter() - t)
+        return best
+    for call in (x.item, sa.sparse_attn_device_error):
+        call()
+    assert least(sa.sparse_attn_device_error) < 3.4 * least(x.item)
