@@ -24,6 +24,20 @@ constexpr int64_t kMaxPlaces = 0x7fffffff - 1024;   // places of a request: the 
 // for 2, 35.1 for 3, 35.4 for 4; a prompt of 2,048 tokens: 84 for 2, 74 for 4, 70 for 6, 69 for 9;
 // 16 x 64 drafts: 193, 181, 176, 177.
 constexpr int kTileCost1 = 3, kTileCost2 = 6;
+// The join's forms (tree_kernel.cuh), by the tiles that the host expects: a block for each row and
+// border at tiles of up to kEachRows rows while there are fewer than kEachTiles; where a tile may be
+// in kFewPieces pieces or more, a block for each row of each tile; else eight rows to a block. The
+// whole call in us, "each", "few" and "wide", bf16, heads of 128, cached tokens behind the @:
+//   1 row, 1 tile @20,000    12.8 14.2 18.4    32 rows, 1 tile @20,000    21.8 14.8 22.0
+//   1 row, 24 tiles @4,000   15.8 17.3 16.8    32 rows, 8 tiles @4,000    20.9 14.3 14.6
+//   4 rows, 1 tile @20,000   13.8 14.8 19.5    32 rows, 10 tiles @1,000   20.3 13.5 12.4
+//   4 rows, 40 tiles @4,000  18.6 20.2 18.9    64 rows, 1 tile @20,000    32.1 15.4 23.5
+//   4 rows, 96 tiles @1,000  20.0 22.1 19.3    128 rows, 9 tiles @20,000  67.8 35.7 37.8
+//   8 rows, 1 tile @20,000   16.3 16.1 21.7    128 rows, 10 tiles @4,000  54.8 23.4 22.7
+//   8 rows, 24 tiles @1,000  14.1 14.1 12.8    two chains, 4 and 5 tiles @4,000: few 23.9, 25.5; wide 24.5, 24.9
+// Over 100,000 tokens tiles of 32, 40, 64 and 128 rows of one head: few 24, 25, 26, 31; wide 51, 52, 54, 59.
+constexpr int kEachRows = 4, kEachTiles = 64, kFewPieces = 32;
+static_assert(2 * kSMs <= 32 * sa::kCutWords, "entries of `cut`");
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
@@ -117,6 +131,7 @@ struct TreeLayout {
   int G, TC, chains;          // query heads of a key head, tokens of a chain, chains of a CTA
   int ctas;                   // CTAs that share the call's key blocks
   bool split;                 // the border between two CTAs' shares may cut a tile
+  int64_t tiles;              // of the call, if no request has more new tokens than expected
   size_t part_o, part_ml, cut, total;
 };
 TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
@@ -130,6 +145,7 @@ TreeLayout tree_layout(const sa_cache& c, const sa_step& s, int Hq) {
   L.TC = std::min(128 / L.G, most);
   L.chains = most > L.TC ? 2 : 1;
   L.ctas = L.chains == 2 ? kSMs : 2 * kSMs;
+  L.tiles = static_cast<int64_t>(s.R) * c.Hkv * ((most - 1) / (L.chains * L.TC) + 1);
   L.split = static_cast<int64_t>(s.width) * c.page_size > sa::kBlock;
   const size_t rows = L.split ? size_t{2} * L.ctas * L.chains * L.TC * L.G : 0;
   size_t o = 0;
@@ -162,17 +178,18 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                          static_cast<long long>(c.head_stride)) != cudaSuccess)
     return SA_ERR_CUDA;
   if (L.split) {
-    // A block for each row where tiles are few and may be in many pieces, else for eight rows,
-    // since most blocks find nothing to do. Blocks of a row against eight, the whole call in us:
-    // 24 rows of one head over 100,000 tokens 28, 50; 30 requests x 32 rows 46, 35; x 4 rows 31.1,
-    // 32.0; 64 requests x 8 heads x 32 rows of up to 1,000 tokens 47, 35.
     const int rows = a.TT * a.G;
-    const int64_t heads = static_cast<int64_t>(a.R) * a.Hkv;
-    const int per = rows <= 32 && (heads < 16 || (rows <= 4 && heads < 64)) ? 1 : 8;
-    cfg.gridDim = dim3(L.ctas, (rows + per - 1) / per);
+    const int form = rows <= kEachRows && L.tiles < kEachTiles ? sa::kJoinEach
+                     : L.tiles * kFewPieces <= L.ctas          ? sa::kJoinFew
+                                                               : sa::kJoinWide;
+    const auto join = form == sa::kJoinEach  ? sa::tree_combine_kernel<D, kElem, 4, sa::kJoinEach>
+                      : form == sa::kJoinFew ? sa::tree_combine_kernel<D, kElem, 4, sa::kJoinFew>
+                                             : sa::tree_combine_kernel<D, kElem, NC == 2 ? 2 : 4, sa::kJoinWide>;
+    cfg.gridDim = dim3(form == sa::kJoinFew ? static_cast<unsigned>(L.tiles) : L.ctas,
+                       form == sa::kJoinWide ? (rows + sa::kCombineRows - 1) / sa::kCombineRows : rows);
     cfg.blockDim = dim3(32 * sa::kCombineWarps);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, sa::tree_combine_kernel<D, kElem, NC == 2 ? 2 : 4>, a, per) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, join, a, L.ctas) != cudaSuccess)
       return SA_ERR_CUDA;
   }
   return SA_OK;

@@ -1151,35 +1151,40 @@ __global__ void __launch_bounds__(TreeCfg<D, NC, kSmallQ>::kThreads, TreeCfg<D, 
 }
 
 // Joins the pieces of the tiles that the shares' borders cut: for each row the largest
-// of the pieces' maxima, then O = sum w_p O_p / sum w_p l_p, w_p = 2^(m_p - m). Block x
-// looks at the tile that CTA x began and did not end, blocks y share its rows. A warp
-// takes a row, or, of a tile in more pieces than warps (few rows, long caches), all warps
-// take one row after another, each every eighth piece; sums in a fixed order either way.
-// Looking for cut tiles from every (token, head) took 89 us for a prompt's chunk of
-// 4,096 x 32 rows of which 148 x 256 are cut; this takes 9.
+// of the pieces' maxima, then O = sum w_p O_p / sum w_p l_p, w_p = 2^(m_p - m), summed in a
+// fixed order. The tile that CTA c began and did not end is in entry c of `cut`. (Looking for
+// cut tiles from every (token, head) took 89 us for a prompt's chunk of 4,096 x 32 rows of which
+// 148 x 256 are cut; this takes 9.)
+// Forms, by what the host expects:
+// kJoinWide: block x looks at entry x, blocks y share its rows, a warp to each. Many tiles, each
+// in few pieces; most blocks find nothing to do.
+// kJoinEach: block (x, y) takes row y of entry x, all warps together, each every eighth piece.
+// Tiles of one to four rows.
+// kJoinFew: as kJoinEach, but blocks x share the cut tiles, looked for through all entries, so
+// that no more blocks are launched than there are rows. Few tiles, each in dozens of pieces.
 // kBatch: pieces that a warp reads at once. Tiles of two chains have many rows in two or three
 // pieces: two, in the registers that let an SM hold all its warps (3 x 500 new tokens behind
-// 1,000, the whole call: 54 us for four, 50 for two). Others have few rows, in up to 296 pieces:
-// four (7 x 13 drafts 18.2 us, for two 20.3).
+// 1,000, the whole call: 54 us for four, 50 for two). Others four (7 x 13 drafts 18.2 us, for two
+// 20.3).
 constexpr int kCombineWarps = 8;
+constexpr int kCombineRows = 8;      // of a block, kJoinWide
+constexpr int kCutWords = 10;        // 32 entries of `cut` each
 
-template <int D, int kElem, int kBatch>
-__global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 1)
-    tree_combine_kernel(const __grid_constant__ TreeArgs a, int rows_per_block) {
+enum JoinForm : int { kJoinWide, kJoinEach, kJoinFew };
+
+template <int D, int kElem, int kBatch, int kForm>
+__global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 4)
+    tree_combine_kernel(const __grid_constant__ TreeArgs a, int ctas) {
   constexpr int kPer = D / 32;                      // elements of a lane
-  __shared__ float s_o[kCombineWarps][D];
-  __shared__ float2 s_ml[kCombineWarps];
+  constexpr bool kTogether = kForm != kJoinWide;    // all warps at one row
+  constexpr int kStep = kTogether ? kCombineWarps : 1;
+  __shared__ float s_o[kTogether ? kCombineWarps : 1][D];
+  __shared__ float2 s_ml[kTogether ? kCombineWarps : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int c0 = static_cast<int>(blockIdx.x);
-  const int4 tile = a.cut[c0];
-  const int row0 = static_cast<int>(blockIdx.y) * rows_per_block, row1 = min(row0 + rows_per_block, tile.y);
-  if (row0 >= row1) return;
-  const int np = tile.w - c0 + 1;
-  const bool shared = rows_per_block == 1;
-  const int step = shared ? kCombineWarps : 1;
-  for (int row = shared ? row0 : row0 + warp; row < row1; row += shared ? 1 : kCombineWarps) {
+  auto join = [&](const int4& tile, int c0, int row) {
+    const int np = tile.w - c0 + 1;
     auto at = [&](int p) { return (2LL * (c0 + p) + (p == 0 ? 1 : 0)) * (a.TT * a.G) + row; };
     float m = -INFINITY, l = 0.f, acc[kPer] = {};
     auto add = [&](float m1, float l1, const float (&v)[kPer]) {   // one more piece
@@ -1190,12 +1195,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 1)
 #pragma unroll
       for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * w0 + v[x] * w1;
     };
-    for (int p0 = shared ? warp : 0; p0 < np; p0 += kBatch * step) {
+    for (int p0 = kTogether ? warp : 0; p0 < np; p0 += kBatch * kStep) {
       float2 ml[kBatch];
       float v[kBatch][kPer];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int p = p0 + u * step;
+        const int p = p0 + u * kStep;
         if (p < np) {
           ml[u] = a.part_ml[at(p)];
           if constexpr (kPer == 4) {
@@ -1207,9 +1212,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 1)
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (p0 + u * step < np) add(ml[u].x, ml[u].y, v[u]);
+        if (p0 + u * kStep < np) add(ml[u].x, ml[u].y, v[u]);
     }
-    if (shared) {
+    if constexpr (kTogether) {
 #pragma unroll
       for (int x = 0; x < kPer; ++x) s_o[warp][lane * kPer + x] = acc[x];
       if (lane == 0) s_ml[warp] = make_float2(m, l);
@@ -1224,7 +1229,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 1)
         }
       }
     }
-    if (!shared || warp == 0) {
+    if (!kTogether || warp == 0) {
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       const long long token = static_cast<long long>(tile.x) + row / a.G;
       const int hq = tile.z * a.G + row % a.G;
@@ -1240,7 +1245,38 @@ __global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 8 : 1)
       if (a.lse && lane == 0)
         a.lse[token * (a.Hkv * a.G) + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    if (shared) __syncthreads();
+    if constexpr (kForm == kJoinFew) __syncthreads();
+  };
+  const int x = static_cast<int>(blockIdx.x), y = static_cast<int>(blockIdx.y);
+  if constexpr (kForm == kJoinWide) {
+    const int4 tile = a.cut[x];
+    const int row0 = y * kCombineRows;
+    for (int row = row0 + warp; row < min(row0 + kCombineRows, tile.y); row += kCombineWarps) join(tile, x, row);
+  } else if constexpr (kForm == kJoinEach) {
+    const int4 tile = a.cut[x];
+    if (y < tile.y) join(tile, x, y);
+  } else {
+    unsigned has[kCutWords];                        // the entries whose tile has row y
+#pragma unroll
+    for (int w = 0; w < kCutWords; ++w) {
+      const int c = w * 32 + lane;
+      has[w] = __ballot_sync(0xffffffffu, c < ctas && a.cut[c].y > y);
+    }
+    for (int k = x;; k += static_cast<int>(gridDim.x)) {
+      int before = 0, c0 = -1;                      // the k-th of them
+#pragma unroll
+      for (int w = 0; w < kCutWords; ++w) {
+        const int n = __popc(has[w]);
+        if (k >= before && k < before + n) {
+          unsigned rest = has[w];
+          for (int i = before; i < k; ++i) rest &= rest - 1;
+          c0 = w * 32 + __ffs(static_cast<int>(rest)) - 1;
+        }
+        before += n;
+      }
+      if (c0 < 0) return;
+      join(a.cut[c0], c0, y);
+    }
   }
 }
 

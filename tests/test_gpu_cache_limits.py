@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged_cache_oracle as orc
-from tests.test_gpu_cache import BF, HF, cache_of, dev_ints, no_device_error
+from tests.test_gpu_cache import BF, HF, cache_of, check_attention, dev_ints, no_device_error, random_mask
 
 pytestmark = pytest.mark.gpu
 
@@ -201,3 +201,52 @@ def test_reading_the_error_word_is_a_launch_and_a_copy():
     for call in (x.item, sa.sparse_attn_device_error):
         call()
     assert least(sa.sparse_attn_device_error) < 3.4 * least(x.item)
+
+
+@pytest.mark.parametrize("R,Hkv,G,T,max_new,d", [
+    (1, 1, 8, 5, 5, 128),       # 40, 64, 128 and 256 rows of one head: a tile in dozens of pieces
+    (1, 1, 64, 1, 1, 64),
+    (1, 1, 8, 16, 16, 128),
+    (1, 1, 4, 64, 64, 64),
+    (1, 4, 8, 9, 9, 128),
+    (9, 1, 33, 1, 1, 64),       # as many tiles as are looked for, and one more
+    (10, 1, 33, 1, 1, 64),
+    (1, 1, 8, 61, 5, 128),      # more tokens than max_new: more cut tiles than blocks for them
+    (2, 2, 5, 40, 3, 64),
+    (1, 1, 4, 300, 65, 64)])
+def test_tiles_in_many_pieces(R, Hkv, G, T, max_new, d):
+    ctx = [6000 - 100 * r for r in range(R)]
+    check_attention(ctx, [T] * R, 64, G * Hkv, Hkv, d, BF, max_new=max_new, seed=T)
+    if max_new == T and R == 1:
+        words = (T + 31) // 32
+        check_attention(ctx, [T], 64, G * Hkv, Hkv, d, HF, max_new=max_new, words=words,
+                        mask=random_mask([T], words, 7, "any"))
+
+
+def test_a_row_more_than_a_warp_costs_no_other_join():
+    """One head's tile over a long cache, in a piece for nearly every CTA: 40 rows take little more
+    than 32 do (a join that reads a row's pieces one after another took 55 us for 33)."""
+    ctx, page, d = 100000, 64, 128
+    kc, vc = (torch.randn(ctx // page + 2, page, 1, d, dtype=BF, device="cuda") for _ in range(2))
+    table = torch.arange(ctx // page + 1, dtype=torch.int32, device="cuda")[None].contiguous()
+    took = {}
+    for T in (4, 5):
+        q = torch.randn(T, 8, d, dtype=BF, device="cuda")
+        plan = sa.CachePlan(table=table, lens=dev_ints([ctx]), starts=dev_ints([0, T]), max_new=T)
+        out = torch.empty_like(q)
+        sa.sparse_attn_tree_fwd(q, kc, vc, plan, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                sa.sparse_attn_tree_fwd(q, kc, vc, plan, out=out)
+        took[T] = math.inf
+        for _ in range(10):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            took[T] = min(took[T], a.elapsed_time(b))
+    no_device_error()
+    assert took[5] < 1.4 * took[4], took
