@@ -9,6 +9,9 @@ and marshalled, the kernels run on the tensors' device and the current torch str
         sparse_attn_cache_write(k, v, plan.slots, k_cache, v_cache)
         o = sparse_attn_tree_fwd(q, k_cache, v_cache, plan)
     sparse_attn_cache_accept(k_caches, v_caches, plan, accepted, taken)
+    lens += taken                            # a step of prompts: lens += plan.granted, no accept
+    held, nfree = plan.held, plan.nfree
+    lens.masked_fill_(new < 0, 0)            # new < 0 ended a request: its row starts anew
 
 A cache is a bf16 or fp16 CUDA tensor [pages, page_size, Hkv, d] (any strides with d
 contiguous, so a transposed [pages, Hkv, page_size, d] fits), pages of 16, 32, 64,
@@ -165,9 +168,10 @@ def sparse_attn_cache_plan(lens: torch.Tensor, new_tokens: torch.Tensor, table: 
 
     lens, new_tokens, held: int32 [R]; table: int32 [R, width] and free_pages: int32
     [pages], both updated in place; nfree: int32 [1]. A negative new_tokens[r] ends request
-    r and returns its pages. n rows are planned (at least the new tokens' sum).
-    mask_words > 0 (32 new tokens to a word) also makes the masks, from parents (int32 [n],
-    each new token's parent among its request's, -1 for none) or for a chain.
+    r and returns its pages; the caller sets its lens to 0. n rows are planned (at least the
+    new tokens' sum). mask_words > 0 (32 new tokens to a word, no request may have more) also
+    makes the masks, from parents (int32 [n], each new token's parent among its request's,
+    -1 for none) or for a chain.
     `out`, a plan of an earlier call of the same sizes, is written again (the plan's held
     and nfree must not be this call's inputs); the returned plan's table, lens and
     free_pages are the ones given."""

@@ -404,7 +404,7 @@ typedef struct {
 typedef struct {
   int32_t R;               /* requests, 1..8192 */
   int32_t n;               /* rows of the step's token buffers */
-  int32_t width;           /* columns of table; R*width, width*page_size <= 2^31 - 1025 */
+  int32_t width;           /* columns of table; R*width < 2^31, width*page_size <= 2^31 - 1025 */
   int32_t max_new;         /* the most new tokens of a request, or 0 if not known (then n / R is
                               taken). It only sizes the tiles: more tokens are still right */
   int32_t words;           /* words of a mask row, 1..32, or 0 with mask = NULL */
@@ -422,7 +422,10 @@ typedef struct {
  *
  *   lens        [R] tokens in the cache
  *   new_tokens  [R] new tokens of the step, 0 included; a negative count means that the
- *               request has ended: its held pages go back on the free list
+ *               request has ended: its held pages go back on the free list, held_out is 0,
+ *               and the caller sets its lens to 0 before the row is used again (a row left
+ *               empty may stay negative; a count of 0 or more with the old lens lacks pages).
+ *               A page must be in one table row only to be returned
  *   held        [R] pages in the request's table row (held*page_size >= lens; a step whose
  *               drafts were not all accepted leaves pages that the next one uses first)
  *   nfree       [1] ids in free_pages
@@ -445,10 +448,14 @@ typedef struct {
  *
  * Not served, with bit 2 set: a request whose counts are out of range (held above width
  * or too few for lens, negative lens, more tokens than width pages or 32*words
- * bits hold, rows past n). A parent out of range ends that walk and sets bit 2. The
- * call may be repeated with the same inputs and gives the same outputs. Errors:
+ * bits hold, rows past n). With masks a step so takes at most 32*words new tokens of a
+ * request, 1,024 at most; longer chunks of prompts go into steps without. nfree out of range
+ * counts as 0, pages returned past the list's end are dropped, a parent out of range ends that
+ * walk: bit 2 as well. A page id outside the pool leaves the token without a slot and sets
+ * bit 1. The call may be repeated with the same inputs and gives the same outputs. Errors:
  * SA_ERR_INVALID_ARG (NULL, misaligned, sizes below 1), SA_ERR_UNSUPPORTED (R > 8192,
- * page_size, a product of sizes above 2^31 - 1), SA_ERR_CUDA. */
+ * page_size, pages*page_size or R*width above 2^31 - 1, width*page_size above 2^31 - 1025),
+ * SA_ERR_CUDA. */
 sa_status sparse_attn_cache_plan(const int32_t* lens, const int32_t* new_tokens, const int32_t* held,
                                  const int32_t* nfree, int32_t* free_pages, int32_t* table, const int32_t* parents,
                                  int32_t R, int32_t pages, int32_t page_size, int32_t width, int32_t n,
@@ -498,7 +505,8 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
  * with a = accepted[r], the rows of K and V at place lens[r] + a[i] go to place lens[r] + i
  * for i < taken[r], in every layer (layer l's caches lie l*layer_stride elements behind the
  * bases). accepted is [R][cols], a[0] < a[1] < ... < the request's new tokens, cols <=
- * 1024; 0 <= taken[r] <= cols. The new length of the request is lens[r] + taken[r]. A
+ * 1024; 0 <= taken[r] <= cols. The new length of the request is lens[r] + taken[r] (of one
+ * whose new tokens all stay, a prompt's, lens[r] + granted[r], without this call). A
  * request whose numbers are out of range (its rows past n among them) keeps its rows of the
  * cache and sets bit 2 (a page id: bit 1).
  * The pages of two requests in one call must differ from place lens on. */

@@ -250,3 +250,45 @@ def test_a_row_more_than_a_warp_costs_no_other_join():
             took[T] = min(took[T], a.elapsed_time(b))
     no_device_error()
     assert took[5] < 1.4 * took[4], took
+
+
+def test_the_documented_loop_with_requests_that_end():
+    """Prompts, drafts, ended requests, empty rows and new prompts in their place, lengths moved on
+    as the README has it: no call flags anything and every page stays in one place."""
+    R, page, Hkv, d, T, width, pages = 4, 16, 1, 64, 6, 12, 40
+    g = torch.Generator().manual_seed(1)
+    caches = [torch.zeros(pages, page, Hkv, d, dtype=BF, device="cuda") for _ in range(2)]
+    lens, held, nfree = dev_ints([0] * R), dev_ints([0] * R), dev_ints([pages])
+    table, free = dev_ints([[0] * width] * R), dev_ints(torch.randperm(pages, generator=g).tolist())
+    want = [0] * R
+
+    def step(new, drafts):
+        nonlocal lens, held, nfree
+        n = max(1, sum(max(t, 0) for t in new))
+        fresh = dev_ints(new)
+        p = sa.sparse_attn_cache_plan(lens, fresh, table, held, free, nfree, n, page, mask_words=1 if drafts else 0)
+        k = torch.randn(n, Hkv, d, generator=g).to(BF).cuda()
+        sa.sparse_attn_cache_write(k, k, p.slots, *caches)
+        sa.sparse_attn_tree_fwd(k.repeat(1, 2, 1), *caches, p)
+        if drafts:
+            taken = [min(max(t, 0), 1 + r) for r, t in enumerate(new)]
+            sa.sparse_attn_cache_accept(*caches, p, dev_ints([list(range(T))] * R), dev_ints(taken))
+            lens += dev_ints(taken)
+        else:
+            taken = [max(t, 0) for t in new]
+            lens += p.granted
+        held, nfree = p.held, p.nfree
+        lens.masked_fill_(fresh < 0, 0)
+        no_device_error()
+        for r, t in enumerate(new):
+            want[r] = 0 if t < 0 else want[r] + taken[r]
+        assert lens.tolist() == want
+        ids = [x for r in range(R) for x in table[r, :int(held[r])].tolist()] + free[:int(nfree)].tolist()
+        assert sorted(ids) == list(range(pages))
+    step([50, 3, 17, 100], False)
+    step([T, T, 1, 0], True)
+    step([T, -1, T, T], True)
+    step([1, -1, T, -1], True)       # an empty row may stay negative
+    step([-1, 0, 2, 0], True)        # or count 0, its length being 0
+    step([30, 40, 5, 0], False)
+    step([T, T, T, -1], True)
