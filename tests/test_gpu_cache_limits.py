@@ -1,13 +1,15 @@
 """Paged cache at the limits its calls state: probabilities far below a row's largest, sizes
 and counts at the ends of their ranges, numbers out of range."""
 import math
+import random
 import time
 
 import pytest
 import torch
 
 from oracle import paged_cache_oracle as orc
-from tests.test_gpu_cache import BF, HF, cache_of, check_attention, dev_ints, no_device_error, random_mask
+from tests.test_gpu_cache import (BF, HF, cache_of, check_attention, check_plan, dev_ints, no_device_error, plan_case,
+                                  random_mask, run_plan)
 
 pytestmark = pytest.mark.gpu
 
@@ -292,3 +294,86 @@ def test_the_documented_loop_with_requests_that_end():
     step([-1, 0, 2, 0], True)        # or count 0, its length being 0
     step([30, 40, 5, 0], False)
     step([T, T, T, -1], True)
+
+
+@pytest.mark.parametrize("R,tree", [(3100, True), (8192, False)])
+def test_plans_of_many_requests(R, tree):
+    """Sums over all requests in more shared memory than a kernel has without asking (48 KB hold
+    some 3,000), up to the most requests of a call."""
+    rng = random.Random(R)
+    c = plan_case(rng, R, 16, tree, R // 10, top_len=60, top_new=20)
+    p = run_plan(c)
+    no_device_error()
+    check_plan(p, c)
+
+
+def test_plan_flags_page_ids_outside_the_pool():
+    """An id on the free list or in a held column that is no page: its tokens get no slot and bit 1
+    is set, all else is as planned."""
+    page, width, pages = 16, 4, 8
+    for where in ("free", "held"):
+        for wrong in (-1, pages, 1 << 30):
+            table = [[0, -5, -5, -5], [1, -5, -5, -5]]
+            free = [2, 3, 4, 5, 6, 7, 0, 0]
+            if where == "free":
+                free[5] = wrong                     # the first one taken
+            else:
+                table[0][0] = wrong
+            t, f = dev_ints(table), dev_ints(free)
+            p = sa.sparse_attn_cache_plan(dev_ints([10, 3]), dev_ints([20, 2]), t, dev_ints([1, 1]), f, dev_ints([6]),
+                                          22, page)
+            torch.cuda.synchronize()
+            assert sa.sparse_attn_device_error() == 2
+            ref = orc.plan([10, 3], [20, 2], [1, 1], 6, free, table, None, page, 22, 0)
+            bad = set(range(6)) if where == "held" else set(range(6, 20))   # places 10..15, 16..29
+            want = [-1 if i in bad else s for i, s in enumerate(ref["slots"])]
+            assert p.slots.tolist() == want and p.granted.tolist() == [20, 2] and int(p.nfree) == ref["nfree"][0]
+            assert p.positions.tolist() == ref["positions"] and p.table[1].tolist() == ref["table"][1]
+
+
+@pytest.mark.parametrize("T,layout", [(257, "nhd"), (1024, "hnd")])
+def test_accept_of_many_rows(T, layout):
+    """More accepted rows than threads, the most of a call, some requests granted fewer, a cache
+    by head."""
+    rng = random.Random(T)
+    page, H, d, R = 32, 2, 64, 3
+    ctx, new, granted = [5, 31, 0], [T + 6] * R, [T + 6, T + 6, 40]
+    kc, vc, table = cache_of(ctx, new, page, H, d, HF, T, layout)
+    taken = [T, 300 if T > 300 else 256, 40]
+    acc = [sorted(rng.sample(range(g), m)) + [0] * (T - m) for g, m in zip(granted, taken)]
+    gpu = lambda x: x.transpose(1, 2).contiguous().cuda().transpose(1, 2) if layout == "hnd" else x.cuda()
+    kg, vg = gpu(kc), gpu(vc)
+    assert kg.stride() == vg.stride() and (layout == "nhd") == kg.is_contiguous()
+    plan = sa.CachePlan(table=dev_ints(table), lens=dev_ints(ctx), starts=dev_ints([(T + 6) * r for r in range(R + 1)]),
+                        granted=dev_ints(granted))
+    sa.sparse_attn_cache_accept(kg, vg, plan, dev_ints(acc), dev_ints(taken))
+    no_device_error()
+    assert torch.equal(kg.cpu(), orc.accept(kc, table, ctx, acc, taken))
+    assert torch.equal(vg.cpu(), orc.accept(vc, table, ctx, acc, taken))
+    # a row that was not granted is none to accept: the request keeps its rows
+    kg, vg = gpu(kc), gpu(vc)
+    acc[2][39] = 40
+    sa.sparse_attn_cache_accept(kg, vg, plan, dev_ints(acc), dev_ints(taken))
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_device_error() == 4
+    assert torch.equal(kg.cpu(), orc.accept(kc, table[:2], ctx[:2], acc, taken))
+
+
+def test_accept_flags_page_ids_outside_the_pool():
+    """A page id that is none, where a row comes from or goes to: the request keeps all its rows,
+    the others move."""
+    ctx, new, page = [14, 14, 14], [40] * 3, 16
+    kc, vc, table = cache_of(ctx, new, page, 2, 64, BF, 9)
+    acc, taken = [[1, 2, 30]] * 3, [3] * 3
+    for column in (0, 2):                           # places 14.. go to pages 0 and 1; 44 comes from page 2
+        for wrong in (-1, kc.shape[0], 1 << 30):
+            t2 = [list(row) for row in table]
+            t2[1][column] = wrong
+            kg, vg = kc.cuda(), vc.cuda()
+            plan = sa.CachePlan(table=dev_ints(t2), lens=dev_ints(ctx), starts=dev_ints([0, 40, 80, 120]))
+            sa.sparse_attn_cache_accept(kg, vg, plan, dev_ints(acc), dev_ints(taken))
+            torch.cuda.synchronize()
+            assert sa.sparse_attn_device_error() == 2
+            rest = [table[0], table[2]]
+            assert torch.equal(kg.cpu(), orc.accept(kc, rest, [14, 14], acc, taken))
+            assert torch.equal(vg.cpu(), orc.accept(vc, rest, [14, 14], acc, taken))
