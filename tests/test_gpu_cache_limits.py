@@ -377,3 +377,38 @@ def test_accept_flags_page_ids_outside_the_pool():
             rest = [table[0], table[2]]
             assert torch.equal(kg.cpu(), orc.accept(kc, rest, [14, 14], acc, taken))
             assert torch.equal(vg.cpu(), orc.accept(vc, rest, [14, 14], acc, taken))
+
+
+def test_attention_of_the_most_requests():
+    rng = random.Random(2)
+    R = 8192
+    ctx = [rng.randint(0, 40) for _ in range(R)]
+    new = [rng.choice([0, 1, 1, 2]) for _ in range(R)]
+    check_attention(ctx, new, 16, 2, 1, 64, BF, max_new=2)
+
+
+def test_places_up_to_the_limit():
+    """Requests of 2^31 - 1025 tokens, nearly all in one page that their tables name again and
+    again; a key in another page (in the middle, and the new token's own) takes the whole softmax."""
+    page, d = 16, 64
+    width = (2 ** 31 - 1025) // page
+    L = width * page - 1
+    kc, vc = (torch.zeros(5, page, 1, d, dtype=BF, device="cuda") for _ in range(2))
+    vc[0] = 1.0
+    table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+    table[0, width // 2 + 1] = 1                    # the peak of the first request
+    kc[1, 5], vc[1, 5] = 8.0, 2.0
+    table[:, width - 1] = dev_ints([2, 3])          # where the new tokens lie, the last place
+    kc[3, 15], vc[2, 15], vc[3, 15] = 8.0, 5.0, 3.0
+    q = torch.ones(2, 1, d, dtype=BF, device="cuda")
+    plan = sa.CachePlan(table=table, lens=dev_ints([L, L]), starts=dev_ints([0, 1, 2]), max_new=1)
+    lse = torch.empty(2, 1, device="cuda")
+    o = sa.sparse_attn_tree_fwd(q, kc, vc, plan, 1.0, lse=lse)
+    no_device_error()
+    # the other scores are 0, the peak's 512: e^-512 is nothing
+    assert torch.all(o[0] == 2.0) and torch.all(o[1] == 3.0)
+    assert torch.all((lse - 512.0).abs() <= 512 * 2.0 ** -22)
+    plan.lens = dev_ints([L + 1, L])                # one place more than the table holds
+    o = sa.sparse_attn_tree_fwd(q, kc, vc, plan, 1.0)
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_device_error() == 4 and torch.all(o[1] == 3.0)
