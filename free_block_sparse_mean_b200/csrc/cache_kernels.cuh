@@ -28,7 +28,9 @@ namespace sa {
 // the returned part of the list is looked up in the ended request's own row, not in
 // the list, and the counts go to outputs apart from the inputs. Measured (one B200, in a
 // captured graph): 64 requests of one token 4 us, 9 prompts of 75,000 tokens 6, 256
-// requests of 48 drafts 11 (a token walks up its tree in up to 48 dependent reads, from L1).
+// requests of 48 drafts in chains 4.2, in trees 6.2 (a token walks up its tree in dependent
+// reads, from L1), with 9 ended ones among them 8.8 and 10.1: one warp returns a request's pages
+// (up to 942), 32 at a time, each a read of the table and then a write of the list.
 struct CachePlanArgs {
   const int *lens, *fresh, *held, *nfree;
   int *free_pages, *table;
@@ -267,9 +269,9 @@ __global__ void __launch_bounds__(kCachePlanThreads) cache_plan_kernel(const Cac
 //
 // cache[slot[i]] = row i, for K and V: 16-byte pieces, each thread four of them at
 // a time so that four loads are in flight. Both caches in one launch (blockIdx.y). Bound
-// by HBM: 29,601 rows of 24 heads of 128, given head by head, take 113 us for 727 MB, 99%
-// of the copy rate. Loads and stores both stream: with stores that stay in L2 until their
-// sector is pushed out the same rows took 151 us. Eight pieces a thread, or a tile of
+// by HBM: 29,601 rows of 24 heads of 128, given head by head, take 110 us (112 a Python call in a
+// loop) for 727 MB, the rate of a copy. Loads and stores both stream: with stores that stay in L2 until their
+// sector is pushed out the same rows took 151 us, and 113 without. Eight pieces a thread, or a tile of
 // tokens with all heads for each CTA (longer runs of a source by head), change nothing.
 struct CacheWriteArgs {
   const uint4* src[2];
@@ -323,8 +325,9 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheWriteArgs a
 // request's moves and takes them in order, eight loads at a time, so no two threads
 // touch the same bytes and nothing has to wait. Rows that stay (acc[i] = i) are
 // neither read nor written. 96 requests that accept up to 9 of 48 drafts in 32 layers of 4
-// heads of 128 take 10 us for some 31 MB (a copy's time: 4.8): lengths, indices and page
-// ids are three reads one after another before the first row.
+// heads of 128 take 8 to 10 us for some 31 MB (a copy's time: 4.8): lengths, indices and page
+// ids are three reads one after another before the first row, and of the 1,536 CTAs four fit
+// on an SM (64 registers; 66 and three made it 9.4 for 8.1), so that is done in 2.6 rounds.
 struct CacheAcceptArgs {
   uint4* cache[2];
   const int *lens, *starts, *granted, *table, *accepted, *taken;

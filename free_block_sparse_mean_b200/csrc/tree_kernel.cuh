@@ -51,16 +51,18 @@
 // softmax waits for P(k-1).V only to correct O. So no wait is ever more than one phase
 // behind its barrier.
 //
-// Measured (one B200, bf16 unless said, in a captured graph): 64 requests of 1..16,384
-// cached tokens, 32 / 8 heads of 128, one token each, fp16: 332 us, 2.2 GB, the copy rate;
-// one request of 4,096, 24 heads: 16 us for 50 MB, bound by its chain of set-up, load,
-// softmax, join; 16 requests x 64 drafted tokens: 153 us, 586 MB and 145 GFLOP; two chunks of
-// 2,048 tokens behind 30,000 and 7,080: 1,113 us, 1,180 TFLOP/s, bound by the chain of a
-// block's softmax and products (in a long loop 1,247 us, at the power limit's clock). Tried and
-// slower or no different, against 1,238 to 1,322 us for the chunks: chains taking turns at the
-// exponentials (1,404), a part of them as polynomials on the FMA pipe (1,406 to 1,469 for
-// one in eight to one in two), exponentials ahead of the block's maximum (1,441), registers
-// split by setmaxnreg (spills).
+// Measured (B200s, bf16 unless said, in replayed graphs from a cool start; in brackets a long
+// loop of calls, where all but the second case may run at the power limit's clock): 64 requests of
+// 1..16,384 cached tokens, 32 / 8 heads of 128, one token each, fp16: 336 us (341 to 375),
+// 2.2 GB, the rate of a copy; one request of 4,096, 24 heads: 16 us (21, the host's) for 50 MB,
+// bound by its chain of set-up, load, softmax, join; 16 requests x 64 drafted tokens: 156 to 171
+// us (180 to 187), 586 MB and 145 GFLOP; two chunks of 2,048 tokens behind 30,000 and 7,080:
+// 1,235 to 1,250 us (1,255), 1,050 TFLOP/s, bound by the chain of a block's softmax and products;
+// with heads of 64 944 us, of which the exponentials are 570. Tried on the chunks and slower or no
+// different, each against the build of its time: chains taking turns at the exponentials
+// (1,238 -> 1,404), a part of them as polynomials on the FMA pipe (1,406 to 1,469 for one in eight
+// to one in two against 1,410 to 1,429, when other things bounded the kernel), exponentials ahead
+// of the block's maximum (1,322 -> 1,441), registers split by setmaxnreg (spills).
 #pragma once
 
 #include <cuda_fp16.h>

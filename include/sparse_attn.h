@@ -477,7 +477,8 @@ sa_status sparse_attn_cache_write(const void* K, const void* V, int64_t token_st
  * cache already (sparse_attn_cache_write). Scores, softmax and sums are fp32; P is
  * rounded to the type for P.V. In fp16 a key of less than 2^-31 of its row's largest
  * probability is lost by that (bf16 has the range of fp32), and |scale q.k| above 4e7 may
- * overflow it.
+ * overflow it. The tensor cores truncate where they add to O: over very long caches a row
+ * loses up to 4e-9 of its size for each key (5e-4 over 131,072).
  *
  *   Q, O       [n][Hq][d] with their strides (elements, multiples of 8), Hq a multiple of
  *              c.Hkv, at most 128 query heads to a key head
