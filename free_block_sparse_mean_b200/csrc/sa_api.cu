@@ -675,18 +675,22 @@ sa_status sparse_attn_device_error(void* stream, int32_t* code) {
   // One small launch and one copy, which waits; a second launch where a code is set. (A read,
   // a clear and a wait for each translation unit's word took 50 us of the host for three of them, 22
   // now, and lost a code that another stream's kernel set between the read and the clear.)
+  auto failed = [] {
+    (void)cudaGetLastError();   // else it fails the next call's check of its launch
+    return SA_ERR_CUDA;
+  };
   void *a = nullptr, *b = nullptr;
   if (sa::noalloc_device_error_word(&a) != cudaSuccess || sa::cache_device_error_word(&b) != cudaSuccess)
-    return SA_ERR_CUDA;
+    return failed();
   sa::gather_device_errors_kernel<<<1, 32, 0, st>>>(static_cast<unsigned int*>(a), static_cast<unsigned int*>(b));
-  if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return failed();
   unsigned int v = 0;
   if (cudaMemcpyFromSymbolAsync(&v, sa::g_dev_error, sizeof(v), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess)
-    return SA_ERR_CUDA;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return SA_ERR_CUDA;
+    return failed();
+  if (cudaStreamSynchronize(st) != cudaSuccess) return failed();
   if (v) {
     sa::clear_device_errors_kernel<<<1, 32, 0, st>>>(v);
-    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) return SA_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) return failed();
   }
   *code = static_cast<int32_t>(v);
   return SA_OK;

@@ -39,6 +39,13 @@ constexpr int kTileCost1 = 3, kTileCost2 = 6;
 constexpr int kEachRows = 4, kEachTiles = 64, kFewPieces = 32;
 static_assert(2 * kSMs <= 32 * sa::kCutWords, "entries of `cut`");
 
+// A failed call of the runtime stays its last error, and would fail the next call's check of
+// its launch, until it is read.
+sa_status cuda_failed() {
+  (void)cudaGetLastError();
+  return SA_ERR_CUDA;
+}
+
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // A stride of a dimension that is stepped over, in elements: positive, 16-byte steps.
@@ -161,7 +168,7 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                       const void* V, const sa_cache& c, const TreeLayout& L, cudaStream_t st) {
   using Cfg = sa::TreeCfg<D, NC, kSmallQ>;
   auto kern = sa::tree_fwd_kernel<D, kElem, NC, kSmallQ>;
-  if (sa::set_smem(kern, Cfg::kSmemBytes) != SA_OK) return SA_ERR_CUDA;
+  if (sa::set_smem(kern, Cfg::kSmemBytes) != SA_OK) return cuda_failed();
   // each kernel sets itself up while the one before it in the stream ends, and waits for that itself
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -176,7 +183,7 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a, static_cast<const uint16_t*>(V),
                          static_cast<long long>(c.page_stride), static_cast<long long>(c.token_stride),
                          static_cast<long long>(c.head_stride)) != cudaSuccess)
-    return SA_ERR_CUDA;
+    return cuda_failed();
   if (L.split) {
     const int rows = a.TT * a.G;
     const int form = rows <= kEachRows && L.tiles < kEachTiles ? sa::kJoinEach
@@ -189,8 +196,7 @@ sa_status launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                        form == sa::kJoinWide ? (rows + sa::kCombineRows - 1) / sa::kCombineRows : rows);
     cfg.blockDim = dim3(32 * sa::kCombineWarps);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, join, a, L.ctas) != cudaSuccess)
-      return SA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, join, a, L.ctas) != cudaSuccess) return cuda_failed();
   }
   return SA_OK;
 }
@@ -231,7 +237,7 @@ sa_status sparse_attn_cache_plan(const int32_t* lens, const int32_t* new_tokens,
     return SA_ERR_UNSUPPORTED;
   const int bytes = (4 * R + 3) * static_cast<int>(sizeof(int));
   if (sa::set_smem(sa::cache_plan_kernel, (4 * sa::kCacheMaxRequests + 3) * static_cast<int>(sizeof(int))) != SA_OK)
-    return SA_ERR_CUDA;
+    return cuda_failed();
   sa::CachePlanArgs a{};
   a.lens = lens;
   a.fresh = new_tokens;

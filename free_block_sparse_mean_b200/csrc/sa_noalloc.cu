@@ -76,7 +76,7 @@ namespace sa {
 // The current GPU's copy of this translation unit's device error word. The
 // plan kernels are templates instantiated here and in the main translation unit;
 // a launch may run either unit's copy, and each copy reports into its own unit's
-// word, so sparse_attn_device_error reads both.
+// word, so sparse_attn_device_error reads them all.
 cudaError_t noalloc_device_error_word(void** word) { return cudaGetSymbolAddress(word, g_dev_error); }
 }  // namespace sa
 

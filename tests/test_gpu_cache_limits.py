@@ -1,5 +1,6 @@
 """Paged cache at the limits its calls state: probabilities far below a row's largest, sizes
 and counts at the ends of their ranges, numbers out of range."""
+import ctypes
 import math
 import random
 import time
@@ -412,3 +413,33 @@ def test_places_up_to_the_limit():
     o = sa.sparse_attn_tree_fwd(q, kc, vc, plan, 1.0)
     torch.cuda.synchronize()
     assert sa.sparse_attn_device_error() == 4 and torch.all(o[1] == 3.0)
+
+
+def test_a_launch_that_fails_fails_no_later_call():
+    """A capture that something else has spoilt: the attention's launch into it is refused, and the
+    calls behind it on the stream, out of the capture again, are not."""
+    rt = ctypes.CDLL("libcudart.so.12")
+    kc, vc, table = cache_of([100], [2], 16, 2, 64, BF, 4, fill=0.0)
+    kc, vc = kc.cuda(), vc.cuda()
+    plan = sa.CachePlan(table=dev_ints(table), lens=dev_ints([100]), starts=dev_ints([0, 2]))
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    want, out = sa.sparse_attn_tree_fwd(q, kc, vc, plan), torch.zeros_like(q)
+    ws = torch.empty(sa.sparse_attn_tree_workspace_size(q, kc, vc, plan), dtype=torch.uint8, device="cuda")
+    slot, row = dev_ints([0]), torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    side = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        assert rt.cudaStreamBeginCapture(handle, 2) == 0             # relaxed
+        assert rt.cudaStreamSynchronize(handle) != 0                 # no wait in a capture: it is spoilt
+        with pytest.raises(sa.SparseAttnError) as e:
+            sa.sparse_attn_tree_fwd(q, kc, vc, plan, out=out, workspace=ws)
+        assert e.value.status == 4
+        with pytest.raises(sa.SparseAttnError):
+            sa.sparse_attn_device_error()
+        assert rt.cudaStreamEndCapture(handle, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+        sa.sparse_attn_cache_write(row, row, slot, kc.clone(), vc.clone())
+        sa.sparse_attn_tree_fwd(q, kc, vc, plan, out=out, workspace=ws)
+    no_device_error()
+    assert torch.equal(out, want)
