@@ -384,6 +384,7 @@ sa_status sparse_attn_cache_accept(void* K_cache, void* V_cache, sa_cache c, int
   if (!aligned(K_cache, 16) || !aligned(V_cache, 16) || !aligned(accepted, 4) || !aligned(taken, 4))
     return SA_ERR_INVALID_ARG;
   if (cols > sa::kAcceptMax) return SA_ERR_UNSUPPORTED;
+  if (K_cache == V_cache) return SA_ERR_INVALID_ARG;   // two threads would move the same rows, each at its own pace
   sa::CacheAcceptArgs a{};
   a.cache[0] = static_cast<uint4*>(K_cache);
   a.cache[1] = static_cast<uint4*>(V_cache);

@@ -510,7 +510,8 @@ sa_status sparse_attn_tree_fwd(const void* Q, int64_t q_token, int64_t q_head, i
  * whose new tokens all stay, a prompt's, lens[r] + granted[r], without this call). A
  * request whose numbers are out of range (its rows past n among them) keeps its rows of the
  * cache and sets bit 2 (a page id: bit 1).
- * The pages of two requests in one call must differ from place lens on. */
+ * The pages of two requests in one call must differ from place lens on, and the caches of
+ * keys and values (one array as both is SA_ERR_INVALID_ARG). */
 sa_status sparse_attn_cache_accept(void* K_cache, void* V_cache, sa_cache c, int32_t layers, int64_t layer_stride,
                                    sa_step s, const int32_t* accepted, int32_t cols, const int32_t* taken,
                                    void* stream);
